@@ -8,9 +8,12 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = [os.path.join(CSRC, "splitzip_kernels.hip"), os.path.join(CSRC, "splitzip_e5m2.hip"),
-           os.path.join(CSRC, "splitzip_host.hip")]
+           os.path.join(CSRC, "splitzip_host.hip"),
+           *(os.path.join(CSRC, f"splitzip_kv4_{part}.hip")
+             for part in ("append", "attend", "weigh", "evict", "host"))]
 HEADERS = [os.path.join(CSRC, "splitzip_internal.h"), os.path.join(CSRC, "splitzip_device.h"),
-           os.path.join(ROOT, "include", "splitzip.h")]
+           os.path.join(CSRC, "splitzip_kv4_internal.h"), os.path.join(CSRC, "splitzip_kv4_tiles.h"),
+           os.path.join(ROOT, "include", "splitzip.h"), os.path.join(ROOT, "include", "splitzip_kv4.h")]
 LIB_PATH = os.path.join(HERE, "libsplitzip.so")
 # streaming read / write / copy kernels that the benchmark times as the achievable ceiling
 CEILING_SOURCES = [os.path.join(CSRC, "stream_ceiling.hip")]

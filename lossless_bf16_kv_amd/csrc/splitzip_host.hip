@@ -929,6 +929,10 @@ int codec_from_codebooks(uint32_t elem, uint32_t n_books, const uint8_t *codeboo
 
 }  // namespace
 
+namespace sz {
+int report(int status, const char *message) { return fail(status, "%s", message); }
+}  // namespace sz
+
 extern "C" {
 
 int splitzip_calibrate_books(uint32_t n_books, const uint16_t *const *d_cal, const uint64_t *n_cal,

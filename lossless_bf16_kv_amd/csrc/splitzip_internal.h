@@ -7,6 +7,9 @@
 
 namespace sz {
 
+// Records a message for splitzip_last_error() and returns the status (splitzip_host.hip).
+int report(int status, const char *message);
+
 // ---- tiling -------------------------------------------------------------------------
 // A workgroup is 4 wave64s.  Each lane owns k*Groups groups of 8 consecutive words (one
 // 16-byte load each); wave w's groups cover 64 * 8 * k*Groups consecutive words.  An encode

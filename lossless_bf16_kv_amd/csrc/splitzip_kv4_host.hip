@@ -1,0 +1,300 @@
+// splitzip_kv4_host.hip -- entry points of the 4-bit KV cache (include/splitzip_kv4.h): argument
+// checks and the choice of launches.
+#include "splitzip_kv4_internal.h"
+
+#include <algorithm>
+#include <cmath>
+#include <stdio.h>
+
+using sz::report;
+using namespace sz::kv4;
+
+namespace {
+
+#define KV4_REQUIRE(cond, message)                           \
+    do {                                                     \
+        if (!(cond))                                         \
+            return report(SPLITZIP_E_INVALID, message);      \
+    } while (0)
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// The cache's device current for the call, and the launch error as the call's status.
+struct Device {
+    int before = -1, status = SPLITZIP_OK;
+    explicit Device(int device)
+    {
+        hipError_t e = hipGetDevice(&before);
+        if (e == hipSuccess && before != device)
+            e = hipSetDevice(device);
+        else
+            before = -1;
+        if (e != hipSuccess)
+            status = failed(e);
+    }
+    ~Device()
+    {
+        if (before >= 0)
+            (void)hipSetDevice(before);
+    }
+    static int failed(hipError_t e)
+    {
+        char text[160];
+        snprintf(text, sizeof text, "4-bit cache launch: %s", hipGetErrorString(e));
+        return report(e == hipErrorOutOfMemory ? SPLITZIP_E_NOMEM : SPLITZIP_E_DEVICE, text);
+    }
+    static int launched()
+    {
+        const hipError_t e = hipGetLastError();
+        return e == hipSuccess ? SPLITZIP_OK : failed(e);
+    }
+};
+
+int check_cache(const splitzip_kv4_cache *c, Cache *out)
+{
+    KV4_REQUIRE(c, "cache is null");
+    KV4_REQUIRE(c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256, "head_dim must be 64, 128 or 256");
+    KV4_REQUIRE(c->kv_heads >= 1 && c->kv_heads <= 65535, "kv_heads must be in [1, 65535]");
+    KV4_REQUIRE(c->page_size >= 16 && c->page_size <= 1024 && (c->page_size & (c->page_size - 1)) == 0,
+                "page_size must be a power of two in [16, 1024]");
+    KV4_REQUIRE(c->num_pages >= 1 && c->num_pages <= INT32_MAX, "num_pages must be in [1, 2^31)");
+    KV4_REQUIRE(c->k_codes && c->k_scales && c->v_codes && c->v_scales && c->weights && c->status,
+                "a cache buffer is null");
+    KV4_REQUIRE(aligned16(c->k_codes) && aligned16(c->k_scales) && aligned16(c->v_codes) && aligned16(c->v_scales) &&
+                    aligned16(c->weights) && (reinterpret_cast<uintptr_t>(c->status) & 3) == 0,
+                "cache buffers must be 16-byte aligned");
+    *out = Cache{c->k_codes, c->k_scales, c->v_codes, c->v_scales, c->weights, c->status, c->num_pages,
+                 __builtin_ctz((unsigned)c->page_size), c->kv_heads};
+    return SPLITZIP_OK;
+}
+
+int check_batch(const splitzip_kv4_batch *b, const Cache &c, bool rows, Batch *out)
+{
+    KV4_REQUIRE(b, "batch is null");
+    KV4_REQUIRE(b->n_seqs >= 0 && b->total >= 0 && b->total < INT32_MAX, "negative or too large batch");
+    KV4_REQUIRE(b->table_width >= 0 && ((int64_t)b->table_width << c.page_shift) <= INT32_MAX - 4096,
+                "table_width is negative or holds 2^31 tokens or more");
+    KV4_REQUIRE(b->n_seqs == 0 || (b->lens && (b->table || b->table_width == 0)), "lens or table is null");
+    KV4_REQUIRE(b->n_seqs <= 1 || b->table_stride >= b->table_width, "table_stride is below table_width");
+    KV4_REQUIRE(!rows || b->cu_seqlens || b->total == b->n_seqs, "without cu_seqlens there is one row a sequence");
+    KV4_REQUIRE(!rows || b->total == 0 || b->n_seqs > 0, "rows without a sequence");
+    KV4_REQUIRE(b->max_q >= 0 && b->max_len >= 0, "max_q or max_len is negative");
+    *out = Batch{b->table, b->lens, b->cu_seqlens, b->table_stride, b->total, b->table_width, b->n_seqs};
+    return SPLITZIP_OK;
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, const splitzip_kv4_cache *c, AttendArgs *a)
+{
+    KV4_REQUIRE(q, "queries is null");
+    KV4_REQUIRE(q->dtype == SPLITZIP_KV4_BF16 || q->dtype == SPLITZIP_KV4_FP16, "queries must be bf16 or fp16");
+    KV4_REQUIRE(q->q_heads >= c->kv_heads && q->q_heads % c->kv_heads == 0, "q_heads must be a multiple of kv_heads");
+    KV4_REQUIRE(b->total * q->q_heads < INT32_MAX, "total * q_heads must be below 2^31");
+    KV4_REQUIRE(q->window >= 0 && q->sinks >= 0, "window or sinks is negative");
+    KV4_REQUIRE(std::isfinite(q->scale), "scale is not finite");
+    KV4_REQUIRE(q->q || b->total == 0, "q is null");
+    KV4_REQUIRE((reinterpret_cast<uintptr_t>(q->q) & 1) == 0, "q is not aligned to its type");
+    a->q = q->q;
+    a->q_token = q->token_stride;
+    a->q_head = q->head_stride;
+    a->q_heads = q->q_heads;
+    a->group = q->q_heads / c->kv_heads;
+    a->window = q->window;
+    a->sinks = q->sinks;
+    a->scale2 = (float)((double)q->scale * 1.4426950408889634);
+    a->wide = aligned16(q->q) && q->token_stride % 8 == 0 && q->head_stride % 8 == 0;
+    return SPLITZIP_OK;
+}
+
+// Launch of an attend call: rows of a workgroup, row tiles, splits along the tokens.
+int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzip_kv4_queries *q, AttendArgs *a,
+         int *tile_rows)
+{
+    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
+    *tile_rows = attend_rows(c->head_dim, q->dtype, rows);
+    const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
+    int64_t tiles = ceil_div(rows, *tile_rows);
+    KV4_REQUIRE(pairs <= INT32_MAX / 4, "too many sequences and heads");
+    tiles = std::min<int64_t>(tiles, std::max<int64_t>(1, INT32_MAX / 4 / std::max<int64_t>(1, pairs)));
+    int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
+    if (q->window > 0)
+        tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
+    const int64_t blocks = std::max<int64_t>(1, pairs * tiles);
+    const int64_t splits = std::min<int64_t>(ceil_div(tokens, 256), 1024 / blocks);
+    a->tiles = (int32_t)tiles;
+    a->splits = (int32_t)std::max<int64_t>(1, splits);
+    return SPLITZIP_OK;
+}
+
+uint64_t workspace_of(const AttendArgs &a, int head_dim)
+{
+    return a.splits == 1 ? 0 : (uint64_t)a.splits * a.b.total * a.q_heads * (head_dim + 2) * 4;
+}
+
+}  // namespace
+
+extern "C" {
+
+int splitzip_kv4_append(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch, const void *k,
+                        int64_t k_token_stride, int64_t k_head_stride, const void *v, int64_t v_token_stride,
+                        int64_t v_head_stride, int32_t dtype, void *stream)
+{
+    AppendArgs a;
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, true, &a.b))
+        return e;
+    KV4_REQUIRE(dtype >= SPLITZIP_KV4_BF16 && dtype <= SPLITZIP_KV4_FP32, "k and v must be bf16, fp16 or fp32");
+    if (a.b.total == 0)
+        return SPLITZIP_OK;
+    KV4_REQUIRE(k && v, "k or v is null");
+    const int size = dtype == SPLITZIP_KV4_FP32 ? 4 : 2;
+    KV4_REQUIRE(reinterpret_cast<uintptr_t>(k) % size == 0 && reinterpret_cast<uintptr_t>(v) % size == 0,
+                "k or v is not aligned to its type");
+    KV4_REQUIRE(a.b.total * a.c.heads < INT32_MAX, "total * kv_heads must be below 2^31");
+    const int unit = 16 / size;
+    a.k = k;
+    a.v = v;
+    a.k_token = k_token_stride;
+    a.k_head = k_head_stride;
+    a.v_token = v_token_stride;
+    a.v_head = v_head_stride;
+    a.wide = aligned16(k) && aligned16(v) && k_token_stride % unit == 0 && k_head_stride % unit == 0 &&
+             v_token_stride % unit == 0 && v_head_stride % unit == 0;
+    Device d(cache->device);
+    if (d.status)
+        return d.status;
+    launch_append(a, cache->head_dim, dtype, static_cast<hipStream_t>(stream));
+    return Device::launched();
+}
+
+int splitzip_kv4_read(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch, void *k, void *v, int32_t dtype,
+                      void *stream)
+{
+    ReadArgs a;
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, true, &a.b))
+        return e;
+    KV4_REQUIRE(dtype >= SPLITZIP_KV4_BF16 && dtype <= SPLITZIP_KV4_FP32, "k and v must be bf16, fp16 or fp32");
+    if (a.b.total == 0)
+        return SPLITZIP_OK;
+    KV4_REQUIRE(k && v && aligned16(k) && aligned16(v), "k or v is null or not 16-byte aligned");
+    KV4_REQUIRE(a.b.total * a.c.heads < INT32_MAX, "total * kv_heads must be below 2^31");
+    a.k = k;
+    a.v = v;
+    Device d(cache->device);
+    if (d.status)
+        return d.status;
+    launch_read(a, cache->head_dim, dtype, static_cast<hipStream_t>(stream));
+    return Device::launched();
+}
+
+int splitzip_kv4_attend_workspace(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
+                                  const splitzip_kv4_queries *queries, uint64_t *bytes)
+{
+    AttendArgs a;
+    int rows;
+    KV4_REQUIRE(bytes, "bytes is null");
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, true, &a.b))
+        return e;
+    if (int e = check_queries(queries, batch, cache, &a))
+        return e;
+    if (int e = plan(cache, batch, queries, &a, &rows))
+        return e;
+    *bytes = workspace_of(a, cache->head_dim);
+    return SPLITZIP_OK;
+}
+
+int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
+                        const splitzip_kv4_queries *queries, void *out, float *lse, void *workspace,
+                        uint64_t workspace_bytes, void *stream)
+{
+    AttendArgs a;
+    int rows;
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, true, &a.b))
+        return e;
+    if (int e = check_queries(queries, batch, cache, &a))
+        return e;
+    if (a.b.total == 0)
+        return SPLITZIP_OK;
+    KV4_REQUIRE(out && aligned16(out), "out is null or not 16-byte aligned");
+    if (int e = plan(cache, batch, queries, &a, &rows))
+        return e;
+    const uint64_t need = workspace_of(a, cache->head_dim);
+    KV4_REQUIRE(need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need),
+                "workspace is missing, misaligned or smaller than splitzip_kv4_attend_workspace says");
+    a.out = out;
+    a.lse = lse;
+    a.part_o = static_cast<float *>(workspace);
+    a.part_ml = a.part_o ? a.part_o + (uint64_t)a.splits * a.b.total * a.q_heads * cache->head_dim : nullptr;
+    Device d(cache->device);
+    if (d.status)
+        return d.status;
+    launch_attend(a, cache->head_dim, queries->dtype, rows, static_cast<hipStream_t>(stream));
+    return Device::launched();
+}
+
+int splitzip_kv4_weigh(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
+                       const splitzip_kv4_queries *queries, const float *lse, void *stream)
+{
+    AttendArgs a;
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, true, &a.b))
+        return e;
+    if (int e = check_queries(queries, batch, cache, &a))
+        return e;
+    if (a.b.total == 0)
+        return SPLITZIP_OK;
+    KV4_REQUIRE(lse, "lse is null");
+    KV4_REQUIRE((int64_t)a.b.n_seqs * a.c.heads <= 1 << 22, "more than 2^22 sequences and heads");
+    a.lse_in = lse;
+    const int64_t cap = (int64_t)a.b.table_width << a.c.page_shift;
+    const int max_len = (int)std::min<int64_t>(batch->max_len, cap);
+    const int max_q = (int)std::max<int64_t>(1, std::min<int64_t>(batch->max_q, batch->total));
+    Device d(cache->device);
+    if (d.status)
+        return d.status;
+    launch_weigh(a, cache->head_dim, queries->dtype, max_q, max_len, static_cast<hipStream_t>(stream));
+    return Device::launched();
+}
+
+int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch, const int32_t *out_table,
+                       int64_t out_table_stride, int32_t out_table_width, int32_t budget, int32_t sinks, int32_t recent,
+                       int32_t *out_lens, int32_t *kept, void *stream)
+{
+    EvictArgs a;
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, false, &a.b))
+        return e;
+    KV4_REQUIRE(budget >= 1 && sinks >= 0 && recent >= 0 && (int64_t)sinks + recent <= budget,
+                "budget must be at least 1 and hold sinks and recent");
+    if (a.b.n_seqs == 0)
+        return SPLITZIP_OK;
+    KV4_REQUIRE(out_table && out_lens && kept, "out_table, out_lens or kept is null");
+    KV4_REQUIRE(out_table_width >= 0 && (a.b.n_seqs <= 1 || out_table_stride >= out_table_width),
+                "out_table_stride is below out_table_width");
+    KV4_REQUIRE((int64_t)a.b.n_seqs * a.c.heads * ceil_div(budget, 16) < INT32_MAX, "too many tokens to keep");
+    a.out_table = out_table;
+    a.out_stride = out_table_stride;
+    a.out_width = out_table_width;
+    a.budget = budget;
+    a.sinks = sinks;
+    a.recent = recent;
+    a.out_lens = out_lens;
+    a.kept = kept;
+    Device d(cache->device);
+    if (d.status)
+        return d.status;
+    launch_evict(a, cache->head_dim, static_cast<hipStream_t>(stream));
+    return Device::launched();
+}
+
+}  // extern "C"

@@ -1,0 +1,244 @@
+// splitzip_kv4_tiles.h -- device code shared by the attention and weight kernels of the 4-bit KV
+// cache: groups of 16 tokens, which of them a block of queries sees, and their conversion to
+// matrix operands.
+//
+// Operands of v_mfma_f32_16x16x32_bf16, of lane l with r = l % 16 and quad = l / 16:
+//   A (16 x 32): row r, columns 8 quad .. + 7;  B (32 x 16): column r, rows 8 quad .. + 7
+//   result (16 x 16): rows 4 quad .. + 3, column r
+// The order in which the 32 terms of a sum are given is free as long as A and B agree, and that
+// makes both products readable straight from the cache:
+//   scores: the sum runs over channels.  A lane holds the D / 4 adjacent channels
+//     quad * D / 4 .. of token r, 8 of them a step: for D = 128 one 16-byte load and one scale.
+//   values: the sum runs over 32 tokens, two groups.  The scores' result already gives a lane
+//     tokens 4 quad .. + 3 of each group for one query, and V's layout gives it, for the same
+//     four tokens, D / 16 adjacent channels; channel r * D / 16 + t is row r of result tile t.
+//     So probabilities never leave their lane and V needs no transposition through memory.
+#pragma once
+
+#include "splitzip_kv4_internal.h"
+
+namespace sz {
+namespace kv4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// x of the other 16-lane rows: the largest (sum) over the four lanes l % 16 = r.
+__device__ __forceinline__ float quad_max(float x)
+{
+    auto a = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+    x = fmaxf(as_float(a[0]), as_float(a[1]));
+    auto b = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+    return fmaxf(as_float(b[0]), as_float(b[1]));
+}
+
+__device__ __forceinline__ float quad_sum(float x)
+{
+    auto a = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+    x = as_float(a[0]) + as_float(a[1]);
+    auto b = __builtin_amdgcn_permlane16_swap(bits(x), bits(x), false, false);
+    return as_float(b[0]) + as_float(b[1]);
+}
+
+__device__ __forceinline__ bf16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const u32x4 v = {a, b, c, d};
+    return __builtin_bit_cast(bf16x8, v);
+}
+
+__device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The groups of 16 tokens that queries at tokens lo .. hi of one sequence see, in token order:
+// first those of the always visible tokens, then those from the window's start to hi.
+struct Groups {
+    int lead, skip, count;       // group v is v for v < lead, else v + skip
+
+    __device__ Groups(int lo, int hi, int window, int sinks)
+    {
+        if (hi < 0) {
+            lead = skip = count = 0;
+            return;
+        }
+        const int from = window > 0 && lo >= window ? (lo - window + 1) >> 4 : 0;
+        lead = min((sinks >> 4) + ((sinks & 15) != 0), from);
+        skip = from - lead;
+        count = (hi >> 4) + 1 - skip;
+    }
+    __device__ int at(int v) const { return v < lead ? v : v + skip; }
+};
+
+// Which tokens queries lo .. hi see.
+struct Mask {
+    int window, sinks;
+    __device__ bool sees(int query, int j) const
+    {
+        return j <= query && (j < sinks || window == 0 || j > query - window);
+    }
+    // every query of lo .. hi sees every token of group g
+    __device__ bool all(int g, int lo, int hi) const
+    {
+        const int j = 16 * g;
+        return j + 15 <= lo && (j + 15 < sinks || window == 0 || j > hi - window);
+    }
+};
+
+// One lane's part of a group's K: D / 8 bytes of codes (channels quad * D / 4 .. of token r) and
+// their scales; of its V: runs r of tokens 4 quad .. + 3 and the scales of those tokens.
+template <int D>
+struct KRaw {
+    uint32_t w[D / 32];
+    uint32_t s;
+};
+template <int D>
+struct VRaw {
+    uint32_t w[D / 32];
+    uint32_t s;
+};
+
+template <int D>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t (&w)[D / 32])
+{
+    if constexpr (D == 64) {
+        const uint2 t = *(const uint2 *)p;
+        w[0] = t.x; w[1] = t.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 128; ++i) {
+            const uint4 t = *(const uint4 *)(p + 16 * i);
+            w[4 * i] = t.x; w[4 * i + 1] = t.y; w[4 * i + 2] = t.z; w[4 * i + 3] = t.w;
+        }
+    }
+}
+
+// Element offset (tokens) of group g of a page and head.
+__device__ __forceinline__ int64_t group_first(const Cache &c, int page, int head, int g)
+{
+    const int64_t p = page < 0 ? 0 : page;
+    return (((p * c.heads + head) << c.page_shift) | ((g << 4) & ((1 << c.page_shift) - 1)));
+}
+
+template <int D>
+__device__ __forceinline__ KRaw<D> load_k(const Cache &c, int page, int head, int g, int lane)
+{
+    const int r = lane & 15, quad = lane >> 4;
+    const int64_t t = group_first(c, page, head, g) + r;
+    KRaw<D> k;
+    load_words<D>(c.k_codes + t * (D / 2) + quad * (D / 8), k.w);
+    const uint8_t *s = c.k_scales + t * (D / 32);
+    if constexpr (D == 64)
+        k.s = s[quad >> 1];
+    else if constexpr (D == 128)
+        k.s = s[quad];
+    else
+        k.s = *(const uint16_t *)(s + 2 * quad);
+    return k;
+}
+
+template <int D>
+__device__ __forceinline__ VRaw<D> load_v(const Cache &c, int page, int head, int g, int lane)
+{
+    const int r = lane & 15, quad = lane >> 4;
+    const int64_t t = group_first(c, page, head, g);
+    VRaw<D> v;
+    load_words<D>(c.v_codes + t * (D / 2) + quad * (2 * D) + r * (D / 8), v.w);
+    const int64_t page0 = t >> c.page_shift << c.page_shift;
+    const int in = (int)(t - page0) + 4 * quad;
+    v.s = *(const uint32_t *)(c.v_scales + page0 * (D / 32) + ((int64_t)(r * (D / 16) / 32) << c.page_shift) + in);
+    return v;
+}
+
+// K operand of step st: channels quad * D / 4 + 8 st .. + 7 of token r.
+template <int D>
+__device__ __forceinline__ bf16x8 k_frag(const KRaw<D> &k, int st)
+{
+    const float s = scale_of(D == 256 ? (st < 4 ? k.s & 0xff : k.s >> 8) : k.s);
+    const uint32_t w = k.w[st];
+    return frag(dequant<0>(w, s), dequant<1>(w, s), dequant<2>(w, s), dequant<3>(w, s));
+}
+
+// Channels 2 p and 2 p + 1 of lane's run, of its token i.
+template <int D>
+__device__ __forceinline__ uint32_t v_pair(const VRaw<D> &v, int i, int p)
+{
+    const float s = scale_of((v.s >> (8 * i)) & 0xff);
+    if constexpr (D == 64) {
+        const uint32_t w = v.w[i >> 1];
+        switch ((i & 1) * 2 + p) {
+        case 0: return dequant<0>(w, s);
+        case 1: return dequant<1>(w, s);
+        case 2: return dequant<2>(w, s);
+        default: return dequant<3>(w, s);
+        }
+    } else {
+        const uint32_t w = v.w[i * (D / 128) + (p >> 2)];
+        switch (p & 3) {
+        case 0: return dequant<0>(w, s);
+        case 1: return dequant<1>(w, s);
+        case 2: return dequant<2>(w, s);
+        default: return dequant<3>(w, s);
+        }
+    }
+}
+
+// The lane's four tokens of channel 2 p (lo) and 2 p + 1 (hi) of its run: half of the V operands
+// of tiles 2 p and 2 p + 1.
+template <int D>
+__device__ __forceinline__ void v_half(const VRaw<D> &v, int p, uint2 &lo, uint2 &hi)
+{
+    const uint32_t a = v_pair<D>(v, 0, p), b = v_pair<D>(v, 1, p), c = v_pair<D>(v, 2, p), d = v_pair<D>(v, 3, p);
+    lo.x = __builtin_amdgcn_perm(b, a, 0x05040100);
+    hi.x = __builtin_amdgcn_perm(b, a, 0x07060302);
+    lo.y = __builtin_amdgcn_perm(d, c, 0x05040100);
+    hi.y = __builtin_amdgcn_perm(d, c, 0x07060302);
+}
+
+// Whether one of the lane's four tokens has a scale past the format's finite ones.
+__device__ __forceinline__ bool v_bad(uint32_t s)
+{
+    return (s & 0xff) > 252 || ((s >> 8) & 0xff) > 252 || ((s >> 16) & 0xff) > 252 || (s >> 24) > 252;
+}
+
+// bf16 pair: elements that are not finite to 0 in x, and to 1 in `is` (others 0).
+__device__ __forceinline__ void split_finite(uint32_t &x, uint32_t &is)
+{
+    const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
+    is = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
+    x &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+}
+
+// Eight channels of a query as bf16 (Half 0: the leading bits, 1: what an fp16 value has beyond
+// them, exact in 3 bits).  bf16 queries have one half.
+template <int T, int Half>
+__device__ __forceinline__ bf16x8 q_frag(const void *q, int64_t at, bool wide)
+{
+    const uint16_t *h = (const uint16_t *)q + at;
+    uint32_t w[4];
+    if (wide) {
+        const uint4 t = *(const uint4 *)h;
+        w[0] = t.x; w[1] = t.y; w[2] = t.z; w[3] = t.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            w[i] = (uint32_t)h[2 * i] | (uint32_t)h[2 * i + 1] << 16;
+    }
+    if constexpr (T == SPLITZIP_KV4_FP16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float a = fp16_of(w[i]), b = fp16_of(w[i] >> 16);
+            const uint32_t top = pack_bf16(a, b);
+            // an infinity stays in the leading half alone: its difference would be a NaN
+            const float x = a - bf16_lo(top), y = b - bf16_hi(top);
+            w[i] = Half == 0 ? top : pack_bf16(x == x ? x : 0.0f, y == y ? y : 0.0f);
+        }
+    }
+    return frag(w[0], w[1], w[2], w[3]);
+}
+
+}  // namespace kv4
+}  // namespace sz
