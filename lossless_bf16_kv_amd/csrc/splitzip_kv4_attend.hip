@@ -82,6 +82,13 @@ __device__ __forceinline__ void share(int count, int splits, int split, int unit
     last = min(count, first + per * unit);
 }
 
+__device__ __forceinline__ bf16x8 flip_sign(bf16x8 x, uint32_t flip)
+{
+    uint4 w = __builtin_bit_cast(uint4, x);
+    w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
+    return __builtin_bit_cast(bf16x8, w);
+}
+
 // Eight probabilities as an operand, in one or two halves.
 template <int Halves>
 __device__ __forceinline__ void p_frag(const float (&p)[8], bf16x8 (&f)[Halves])
@@ -98,42 +105,6 @@ __device__ __forceinline__ void p_frag(const float (&p)[8], bf16x8 (&f)[Halves])
             x[i] = pack_bf16(p[2 * i] - bf16_lo(w[i]), p[2 * i + 1] - bf16_hi(w[i]));
         f[1] = frag(x[0], x[1], x[2], x[3]);
     }
-}
-
-// 1 where the query sees the token, as an operand like p_frag's.
-__device__ __forceinline__ bf16x8 seen_frag(const Mask &mask, int query, int ja, int jb, bool ga, bool gb)
-{
-    uint32_t w[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        w[i] = (ga && mask.sees(query, ja + 2 * i) ? 0x3f80u : 0u) | (ga && mask.sees(query, ja + 2 * i + 1) ? 0x3f800000u : 0u);
-        w[2 + i] = (gb && mask.sees(query, jb + 2 * i) ? 0x3f80u : 0u) | (gb && mask.sees(query, jb + 2 * i + 1) ? 0x3f800000u : 0u);
-    }
-    return frag(w[0], w[1], w[2], w[3]);
-}
-
-// o += V^T p over two groups for one result tile.  `odd`: some V among them is not finite and not
-// every row sees all of them.  A product with a probability of 0 would be a NaN there, so such
-// values are left out and the rows that do see one get a NaN.
-template <int Halves>
-__device__ __forceinline__ f32x4 add_pv(uint2 a, uint2 b, const bf16x8 (&p)[Halves], f32x4 o, bool odd, bf16x8 seen)
-{
-    if (odd) {
-        uint2 ia, ib;
-        split_finite(a.x, ia.x);
-        split_finite(a.y, ia.y);
-        split_finite(b.x, ib.x);
-        split_finite(b.y, ib.y);
-        const f32x4 hit = mfma(frag(ia.x, ia.y, ib.x, ib.y), seen, f32x4{0, 0, 0, 0});
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            o[i] = hit[i] > 0.0f ? NAN : o[i];
-    }
-    const bf16x8 v = frag(a.x, a.y, b.x, b.y);
-    o = mfma(v, p[0], o);
-    if constexpr (Halves == 2)
-        o = mfma(v, p[1], o);
-    return o;
 }
 
 // ---- few rows -------------------------------------------------------------------------------
@@ -182,6 +153,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
         share(groups.count, a.splits, at.split, 8, first, last);
 
         float m = -INFINITY, l = 0.0f;
+        uint32_t lost = 0;                       // blocks whose result is a NaN
         f32x4 o[kTiles];
 #pragma unroll
         for (int t = 0; t < kTiles; ++t)
@@ -195,8 +167,8 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
             const int pb = p.gb < 0 ? -1 : page_of(a.c, a.b, at.s, 16 * p.gb);
             p.ka = load_k<D>(a.c, pa, at.head, p.ga, lane);
             p.kb = load_k<D>(a.c, pb, at.head, p.gb, lane);
-            p.va = load_v<D>(a.c, pa, at.head, p.ga, lane);
-            p.vb = load_v<D>(a.c, pb, at.head, p.gb, lane);
+            p.va = load_v<D>(a.c, pa, at.head, p.ga, lane, quad);
+            p.vb = load_v<D>(a.c, pb, at.head, p.gb, lane, quad);
             p.ga = pa < 0 ? -1 : p.ga;
             p.gb = pb < 0 ? -1 : p.gb;
             return p;
@@ -206,7 +178,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
         if (v < last)
             next = fetch(v);
         for (; v < last; v += 8) {
-            const Pair<D> cur = next;
+            Pair<D> cur = next;
             if (v + 8 < last)
                 next = fetch(v + 8);
             f32x4 sa = {0, 0, 0, 0}, sb = {0, 0, 0, 0};
@@ -257,18 +229,33 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
             }
             bf16x8 pf[kHalves];
             p_frag<kHalves>(p, pf);
-            bf16x8 seen = {};
-            const bool odd = !whole && __any(v_bad(cur.va.s) || v_bad(cur.vb.s));
-            if (odd)
-                seen = seen_frag(mask, query, ja, jb, cur.ga >= 0, cur.gb >= 0);
+            if (!whole && __any(v_bad(cur.va.s) || v_bad(cur.vb.s))) {
+                no_nan(cur.va);
+                no_nan(cur.vb);
+                lost |= poison<D>(a.c, a.b, at.s, at.head, cur.ga, mask, query);
+                lost |= poison<D>(a.c, a.b, at.s, at.head, cur.gb, mask, query);
+            }
 #pragma unroll
             for (int t = 0; t < kTiles; t += 2) {
                 uint2 a0, a1, b0, b1;
                 v_half<D>(cur.va, t / 2, a0, a1);
                 v_half<D>(cur.vb, t / 2, b0, b1);
-                o[t] = add_pv<kHalves>(a0, b0, pf, o[t], odd, seen);
-                o[t + 1] = add_pv<kHalves>(a1, b1, pf, o[t + 1], odd, seen);
+                const bf16x8 f0 = frag(a0.x, a0.y, b0.x, b0.y), f1 = frag(a1.x, a1.y, b1.x, b1.y);
+#pragma unroll
+                for (int h = 0; h < kHalves; ++h) {
+                    o[t] = mfma(f0, pf[h], o[t]);
+                    o[t + 1] = mfma(f1, pf[h], o[t + 1]);
+                }
             }
+        }
+        if (__any(lost != 0)) {
+            // the lane's channels (4 quad + i) * kTiles + t: of block (4 quad + i) / 2
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (lost >> ((4 * quad + i) * kTiles / 32) & 1)
+#pragma unroll
+                    for (int t = 0; t < kTiles; ++t)
+                        o[t][i] = NAN;
         }
 
         // join the four waves
@@ -333,27 +320,50 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
 
 // ---- many rows ------------------------------------------------------------------------------
 
-// A workgroup of 4 waves takes 64 * Cols rows, 16 * Cols a wave, and 64 tokens a turn.  LDS holds
-// the operands of two turns, each in the order in which lanes read it, so reads need no swizzle:
-//   K: [group 4][step][lane] 16 bytes;  V: [pair of groups 2][tile][half 2][lane] 8 bytes
-template <int D, int T, int Cols>
-__global__ __launch_bounds__(kLanes, D == 256 || Cols * (T == SPLITZIP_KV4_FP16 ? 2 : 1) > 2 ? 1 : 2) void many_rows(AttendArgs a)
+// kWaves waves, 32 rows each: `Rows` of them side by side along the rows, the others (times Rows)
+// take other tokens of a turn and are joined at the end.  A turn is 16 tokens a wave: each wave puts
+// the codes and scales of one group's K and the bf16 operands of its V into LDS, all in the order in
+// which lanes read them, and every wave multiplies tiles of 32 tokens from there.  V's conversion
+// is shared, since it takes two instructions a value pair and a transposition; K's takes one, and its
+// codes are a quarter of the LDS traffic that bf16 would be.
+template <int D>
+struct Stage {
+    static constexpr int kWaves = D == 256 ? 4 : 8;
+    static constexpr int kTiles = kWaves / 2;            // of 32 tokens, a turn
+    static constexpr int kLaneScales = D / 64;           // K's scale bytes of a lane: of D / 2 channels
+    uint4 k[kTiles][D / 64][64];                         // lane (token l % 32): channels (l / 32) D / 2 ..
+    uint4 v[kWaves][D / 32][64];                         // lane (channel): tokens 8 j + 4 (l / 32) .. + 3, j < 2
+    uint8_t ks[kTiles][64][kLaneScales];
+    int group[kWaves];                                   // -1: none
+    int bad[kWaves];                                     // V of the group is not finite
+};
+
+template <int D, int T, int Rows>
+__global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_rows(AttendArgs a)
 {
     constexpr int kHalves = T == SPLITZIP_KV4_FP16 ? 2 : 1;
-    constexpr int kSteps = D / 32, kTiles = D / 16;
-    constexpr int kRows = 64 * Cols;
-    __shared__ uint4 sh_k[2 * 4 * kSteps * 64];
-    __shared__ uint2 sh_v[2 * 2 * kTiles * 2 * 64];
-    __shared__ int sh_bad[2][4];     // a wave's group has V that is not finite
-    __shared__ int sh_group[2][4];   // its group, -1: none
+    constexpr int kWaves = Stage<D>::kWaves, kTiles = Stage<D>::kTiles;
+    constexpr int kSteps = D / 16, kOut = D / 32;
+    constexpr int kParts = kWaves / Rows;                // waves that share rows
+    constexpr int kRows = 32 * Rows;
+    static_assert(kParts <= kTiles, "a wave without a tile");
+    __shared__ union Shared {
+        Stage<D> stage[2];
+        float join[kParts > 1 ? kWaves / 2 : 1][16 * kOut + 2][64];
+        __device__ Shared() {}
+    } sh;
 
     const Place at(a);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, quad = lane >> 4;
+    const int m32 = lane & 31, half = lane >> 5;
+    const int part = wave / Rows;
     fill_unowned<D>(a, at);
     const Seq q = sequence(a.c, a.b, at.s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
+    // scores are scaled by |scale|: a negative one is in the queries' signs
+    const float scale = fabsf(a.scale2);
+    const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;
 
     // later rows see more tokens: they start first
     const int row_tiles = (rows + kRows - 1) / kRows;
@@ -362,199 +372,247 @@ __global__ __launch_bounds__(kLanes, D == 256 || Cols * (T == SPLITZIP_KV4_FP16 
         const int base = q.len - q.n;
         const Groups groups(base + row0 / a.group, base + min(row0 + kRows - 1, rows - 1) / a.group, a.window, a.sinks);
         int first, last;
-        share(groups.count, a.splits, at.split, 4, first, last);
+        share(groups.count, a.splits, at.split, kWaves, first, last);
 
         // this wave's rows; a row past the end repeats the last and is not stored
-        const int w_row = row0 + wave * 16 * Cols;
-        int query[Cols];
-        bf16x8 qf[kHalves][Cols][kSteps];
-#pragma unroll
-        for (int c = 0; c < Cols; ++c) {
-            const int row = min(w_row + 16 * c + r, rows - 1);
-            query[c] = base + row / a.group;
+        const int w_row = row0 + wave % Rows * 32;
+        const int row = min(w_row + m32, rows - 1);
+        const int query = base + row / a.group;
+        bf16x8 qf[kHalves][kSteps];
+        {
             const int64_t p0 = (q.row0 + row / a.group) * a.q_token + (at.head * a.group + row % a.group) * a.q_head +
-                               quad * (D / 4);
+                               half * (D / 2);
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
-                qf[0][c][st] = q_frag<T, 0>(a.q, p0 + 8 * st, a.wide);
+                qf[0][st] = flip_sign(q_frag<T, 0>(a.q, p0 + 8 * st, a.wide), flip);
                 if constexpr (kHalves == 2)
-                    qf[1][c][st] = q_frag<T, 1>(a.q, p0 + 8 * st, a.wide);
+                    qf[1][st] = flip_sign(q_frag<T, 1>(a.q, p0 + 8 * st, a.wide), flip);
             }
         }
         const int q_lo = base + min(w_row, rows - 1) / a.group;
-        const int q_hi = base + min(w_row + 16 * Cols - 1, rows - 1) / a.group;
+        const int q_hi = base + min(w_row + 31, rows - 1) / a.group;
 
-        float m[Cols], l[Cols];
-        f32x4 o[Cols][kTiles];
+        float m = -INFINITY, l = 0.0f;
+        uint32_t lost = 0;                               // blocks whose result is a NaN
+        f32x16 o[kOut];
 #pragma unroll
-        for (int c = 0; c < Cols; ++c) {
-            m[c] = -INFINITY;
-            l[c] = 0.0f;
-#pragma unroll
-            for (int t = 0; t < kTiles; ++t)
-                o[c][t] = f32x4{0, 0, 0, 0};
-        }
+        for (int t = 0; t < kOut; ++t)
+            o[t] = f32x16{};
 
         struct Raw {
             KRaw<D> k;
             VRaw<D> v;
             int g;
         } raw;
+        const int r = lane & 15, quad = lane >> 4;
+        // the four tokens whose V a lane converts: lanes 0 .. 31 then write 256 adjacent bytes
+        const int v_quad = 2 * (quad & 1) + (quad >> 1);
         auto fetch = [&](int v) {
             Raw x;
             x.g = v < last ? groups.at(v) : -1;
             const int page = x.g < 0 ? -1 : page_of(a.c, a.b, at.s, 16 * x.g);
             x.k = load_k<D>(a.c, page, at.head, x.g, lane);
-            x.v = load_v<D>(a.c, page, at.head, x.g, lane);
+            x.v = load_v<D>(a.c, page, at.head, x.g, lane, v_quad);
             x.g = page < 0 ? -1 : x.g;
             return x;
         };
-        auto convert = [&](const Raw &x, int buf) {
-            uint4 *k = sh_k + (buf * 4 + wave) * kSteps * 64 + lane;
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st)
-                k[st * 64] = __builtin_bit_cast(uint4, k_frag<D>(x.k, st));
-            uint2 *v = sh_v + ((buf * 2 + wave / 2) * kTiles * 2 + wave % 2) * 64 + lane;
-#pragma unroll
-            for (int t = 0; t < kTiles; t += 2) {
-                uint2 lo, hi;
-                v_half<D>(x.v, t / 2, lo, hi);
-                v[t * 128] = lo;
-                v[(t + 1) * 128] = hi;
-            }
+        auto put = [&](Raw &x, Stage<D> &st) {
             const bool bad = __any(v_bad(x.v.s));
+            if (bad)
+                no_nan(x.v);
+            const int to = (quad >> 1) * 32 + (wave & 1) * 16 + r;      // K's lane; its piece is of the half's second half
+            if constexpr (D == 64) {
+                *(uint2 *)((char *)&st.k[wave / 2][0][to] + 8 * (quad & 1)) = make_uint2(x.k.w[0], x.k.w[1]);
+                if ((quad & 1) == 0)
+                    st.ks[wave / 2][to][0] = (uint8_t)x.k.s;
+            } else {
+#pragma unroll
+                for (int i = 0; i < D / 128; ++i)
+                    st.k[wave / 2][(quad & 1) * (D / 128) + i][to] =
+                        make_uint4(x.k.w[4 * i], x.k.w[4 * i + 1], x.k.w[4 * i + 2], x.k.w[4 * i + 3]);
+                if constexpr (D == 128)
+                    st.ks[wave / 2][to][quad & 1] = (uint8_t)x.k.s;
+                else
+                    *(uint16_t *)&st.ks[wave / 2][to][2 * (quad & 1)] = (uint16_t)x.k.s;
+            }
+#pragma unroll
+            for (int t = 0; t < kOut; ++t) {
+                uint2 lo, hi;
+                v_half<D>(x.v, t, lo, hi);
+                uint2 *v = (uint2 *)&st.v[wave][t][(quad >> 1) * 32 + r] + (quad & 1);
+                v[0] = lo;
+                v[32] = hi;                              // 16 lanes on
+            }
             if (lane == 0) {
-                sh_bad[buf][wave] = bad;
-                sh_group[buf][wave] = x.g;
+                st.bad[wave] = bad;
+                st.group[wave] = x.g;
             }
         };
 
         if (first < last) {
             raw = fetch(first + wave);
-            convert(raw, 0);
-            raw = fetch(first + 4 + wave);
+            put(raw, sh.stage[0]);
+            raw = fetch(first + kWaves + wave);
         }
         __syncthreads();
         int buf = 0;
-        for (int v = first; v < last; v += 4, buf ^= 1) {
-            if (v + 4 < last) {
-                convert(raw, buf ^ 1);
-                raw = fetch(v + 8 + wave);
+        for (int v = first; v < last; v += kWaves, buf ^= 1) {
+            const Stage<D> &st = sh.stage[buf];
+            if (v + kWaves < last) {
+                put(raw, sh.stage[buf ^ 1]);
+                raw = fetch(v + 2 * kWaves + wave);
             }
-            int g[4];
-            bool whole = true, bad = false, any = false;
+#pragma unroll 1
+            for (int tile = part; tile < kTiles; tile += kParts) {
+                const int ga = __builtin_amdgcn_readfirstlane(st.group[2 * tile]);
+                const int gb = __builtin_amdgcn_readfirstlane(st.group[2 * tile + 1]);
+                if (!((ga >= 0 && 16 * ga <= q_hi) || (gb >= 0 && 16 * gb <= q_hi)))
+                    continue;
+                const bool whole = ga >= 0 && gb >= 0 && mask.all(ga, q_lo, q_hi) && mask.all(gb, q_lo, q_hi);
+                // scores of 32 tokens
+                f32x16 x = {};
+                {
+                    uint32_t s = 0;
+                    if constexpr (D == 64)
+                        s = st.ks[tile][lane][0];
+                    else if constexpr (D == 128)
+                        s = *(const uint16_t *)st.ks[tile][lane];
+                    else
+                        s = *(const uint32_t *)st.ks[tile][lane];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                g[i] = __builtin_amdgcn_readfirstlane(sh_group[buf][i]);
-                whole = whole && g[i] >= 0 && mask.all(g[i], q_lo, q_hi);
-                any = any || (g[i] >= 0 && 16 * g[i] <= q_hi);
-                bad = bad || __builtin_amdgcn_readfirstlane(sh_bad[buf][i]) != 0;
-            }
-            if (any) {
-                // scores of 64 tokens
-                f32x4 x[Cols][4];
+                    for (int p = 0; p < D / 64; ++p) {
+                        const uint4 c = st.k[tile][p][lane];
+                        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+                        const float ks = scale_of((s >> (8 * p)) & 0xff);       // 32 channels: one block
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-#pragma unroll
-                    for (int c = 0; c < Cols; ++c)
-                        x[c][i] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                    for (int st = 0; st < kSteps; ++st) {
-                        const bf16x8 f = __builtin_bit_cast(bf16x8, sh_k[((buf * 4 + i) * kSteps + st) * 64 + lane]);
-#pragma unroll
-                        for (int c = 0; c < Cols; ++c)
+                        for (int i = 0; i < 4; ++i) {
+                            const bf16x8 f = frag(dequant<0>(w[i], ks), dequant<1>(w[i], ks), dequant<2>(w[i], ks),
+                                                  dequant<3>(w[i], ks));
 #pragma unroll
                             for (int h = 0; h < kHalves; ++h)
-                                x[c][i] = mfma(f, qf[h][c][st], x[c][i]);
+                                x = mfma32(f, qf[h][4 * p + i], x);
+                        }
                     }
                 }
-                bf16x8 pf[Cols][2][kHalves];
+                if (!whole) {
 #pragma unroll
-                for (int c = 0; c < Cols; ++c) {
-                    float top = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float y = x[c][i][e] * a.scale2;
-                            if (!whole)
-                                y = g[i] >= 0 && mask.sees(query[c], 16 * g[i] + 4 * quad + e) ? y : -INFINITY;
-                            x[c][i][e] = y;
-                            top = fmaxf(top, y);
-                        }
-                    top = quad_max(top);
-                    if (__any(top > m[c] + 8.0f)) {
-                        const float grown = fmaxf(m[c], top);
-                        const float f = grown == -INFINITY ? 1.0f : exp2_fast(m[c] - grown);
-                        m[c] = grown;
-                        l[c] *= f;
-#pragma unroll
-                        for (int t = 0; t < kTiles; ++t)
-                            o[c][t] *= f;
-                    }
-                    const float ref = m[c] == -INFINITY ? 0.0f : m[c];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float p[8];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            p[e] = exp2_fast(x[c][2 * h + e / 4][e % 4] - ref);
-                            l[c] += p[e];
-                        }
-                        p_frag<kHalves>(p, pf[c][h]);
+                    for (int e = 0; e < 16; ++e) {
+                        const int g = e < 8 ? ga : gb;
+                        const int j = 16 * g + 8 * ((e >> 2) & 1) + 4 * half + (e & 3);
+                        x[e] = g >= 0 && mask.sees(query, j) ? x[e] : -INFINITY;
                     }
                 }
-                const bool odd = bad && !whole;
+                float top = x[0];
+#pragma unroll
+                for (int e = 1; e < 16; ++e)
+                    top = fmaxf(top, x[e]);
+                top = half_max(top) * scale;
+                if (__any(top > m + 8.0f)) {
+                    const float grown = fmaxf(m, top);
+                    const float f = grown == -INFINITY ? 1.0f : exp2_fast(m - grown);
+                    m = grown;
+                    l *= f;
+#pragma unroll
+                    for (int t = 0; t < kOut; ++t)
+                        o[t] *= f;
+                }
+                const float ref = m == -INFINITY ? 0.0f : m;
+                bf16x8 pf[2][kHalves];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    bf16x8 seen[Cols] = {};
-                    if (odd)
+                    float p[8];
 #pragma unroll
-                        for (int c = 0; c < Cols; ++c)
-                            seen[c] = seen_frag(mask, query[c], 16 * g[2 * h] + 4 * quad, 16 * g[2 * h + 1] + 4 * quad,
-                                                g[2 * h] >= 0, g[2 * h + 1] >= 0);
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t) {
-                        const uint2 *v2 = sh_v + ((buf * 2 + h) * kTiles + t) * 128 + lane;
-                        const uint2 va = v2[0], vb = v2[64];
-#pragma unroll
-                        for (int c = 0; c < Cols; ++c)
-                            o[c][t] = add_pv<kHalves>(va, vb, pf[c][h], o[c][t], odd, seen[c]);
+                    for (int e = 0; e < 8; ++e) {
+                        p[e] = exp2_fast(fmaf(x[8 * h + e], scale, -ref));
+                        if (!whole)
+                            p[e] = x[8 * h + e] == -INFINITY ? 0.0f : p[e];     // also where the scale is 0
+                        l += p[e];
                     }
+                    p_frag<kHalves>(p, pf[h]);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int t = 0; t < kOut; ++t) {
+                        const bf16x8 y = __builtin_bit_cast(bf16x8, st.v[2 * tile + h][t][lane]);
+#pragma unroll
+                        for (int i = 0; i < kHalves; ++i)
+                            o[t] = mfma32(y, pf[h][i], o[t]);
+                    }
+                if (__builtin_amdgcn_readfirstlane(st.bad[2 * tile] | st.bad[2 * tile + 1])) {
+                    lost |= poison<D>(a.c, a.b, at.s, at.head, ga, mask, query);
+                    lost |= poison<D>(a.c, a.b, at.s, at.head, gb, mask, query);
                 }
             }
             __syncthreads();
         }
+        l = half_sum(l);
+        if (__any(lost != 0)) {
+            // run 8 i + 4 half + e of D / 16 channels: block run / 2
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (lost >> ((8 * (i >> 2) + 4 * half + (i & 3)) * (D / 16) / 32) & 1)
+#pragma unroll
+                    for (int t = 0; t < kOut; ++t)
+                        o[t][i] = o[t][8 + i] = NAN;
+        }
 
+        // join the waves of the same rows, half of the parts to the other half
+        if constexpr (kParts > 1) {
 #pragma unroll
-        for (int c = 0; c < Cols; ++c) {
-            const int row = w_row + 16 * c + r;
-            const float sum = quad_sum(l[c]);
-            if (row >= rows)
-                continue;
+            for (int d = kParts / 2; d >= 1; d /= 2) {
+                float (*const x)[64] = sh.join[wave % (d * Rows)];
+                if (part >= d && part < 2 * d) {
+#pragma unroll
+                    for (int t = 0; t < kOut; ++t)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            x[16 * t + e][lane] = o[t][e];
+                    x[16 * kOut][lane] = m;
+                    x[16 * kOut + 1][lane] = l;
+                }
+                __syncthreads();
+                if (part < d) {
+                    const float m2 = x[16 * kOut][lane], big = fmaxf(m, m2);
+                    const float f = big == -INFINITY ? 1.0f : exp2_fast(m - big);
+                    const float f2 = big == -INFINITY ? 1.0f : exp2_fast(m2 - big);
+                    m = big;
+                    l = l * f + x[16 * kOut + 1][lane] * f2;
+#pragma unroll
+                    for (int t = 0; t < kOut; ++t)
+#pragma unroll
+                        for (int e = 0; e < 16; ++e)
+                            o[t][e] = o[t][e] * f + x[16 * t + e][lane] * f2;
+                }
+                __syncthreads();
+            }
+        }
+        if (part == 0 && w_row + m32 < rows) {
             const int64_t gr = (q.row0 + row / a.group) * (int64_t)a.q_heads + at.head * a.group + row % a.group;
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            // run 8 i + 4 half + e of D / 16 channels, for this lane's row
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 8; ++i) {
+                const int d = (8 * (i >> 2) + 4 * half + (i & 3)) * (D / 16);
 #pragma unroll
-                for (int t = 0; t < kTiles; t += 4) {
-                    const int d = (4 * quad + i) * kTiles + t;
-                    f32x4 x = {o[c][t][i], o[c][t + 1][i], o[c][t + 2][i], o[c][t + 3][i]};
+                for (int c = 0; c < D / 16; c += 4) {
+                    f32x4 y = {o[c / 2][i], o[c / 2][8 + i], o[c / 2 + 1][i], o[c / 2 + 1][8 + i]};
                     if (a.splits == 1) {
-                        x *= inv;
-                        *(uint2 *)((uint16_t *)a.out + gr * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
+                        y *= inv;
+                        *(uint2 *)((uint16_t *)a.out + gr * D + d + c) = make_uint2(to_type(y[0], y[1], T), to_type(y[2], y[3], T));
                     } else {
-                        *(f32x4 *)(a.part_o + ((int64_t)at.split * a.b.total * a.q_heads + gr) * D + d) = x;
+                        *(f32x4 *)(a.part_o + ((int64_t)at.split * a.b.total * a.q_heads + gr) * D + d + c) = y;
                     }
                 }
-            if (quad == 0) {
+            }
+            if (half == 0) {
                 if (a.splits == 1) {
                     if (a.lse)
-                        a.lse[gr] = sum == 0.0f ? -INFINITY : (m[c] + __log2f(sum)) * kLn2;
+                        a.lse[gr] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
                 } else {
                     float *ml = a.part_ml + ((int64_t)at.split * a.b.total * a.q_heads + gr) * 2;
-                    ml[0] = m[c];
-                    ml[1] = sum;
+                    ml[0] = m;
+                    ml[1] = l;
                 }
             }
         }
@@ -596,12 +654,15 @@ template <int D, int T>
 void attend_dt(const AttendArgs &a, int tile_rows, hipStream_t s)
 {
     const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.tiles * a.splits);
+    constexpr int kLanesMany = 64 * Stage<D>::kWaves;
     if (tile_rows == 16)
         few_rows<D, T><<<grid, kLanes, 0, s>>>(a);
     else if (tile_rows == 64)
-        many_rows<D, T, 1><<<grid, kLanes, 0, s>>>(a);
-    else if constexpr (D < 256 || T == SPLITZIP_KV4_BF16)
-        many_rows<D, T, 2><<<grid, kLanes, 0, s>>>(a);
+        many_rows<D, T, 2><<<grid, kLanesMany, 0, s>>>(a);
+    else if (tile_rows == 128)
+        many_rows<D, T, 4><<<grid, kLanesMany, 0, s>>>(a);
+    else if constexpr (D < 256)
+        many_rows<D, T, 8><<<grid, kLanesMany, 0, s>>>(a);
     if (a.splits > 1) {
         constexpr int kRows = kLanes / (D / 4);
         join_kernel<D, T><<<(unsigned)((a.b.total * a.q_heads + kRows - 1) / kRows), kLanes, 0, s>>>(a);
@@ -619,11 +680,9 @@ void attend_d(const AttendArgs &a, int dtype, int tile_rows, hipStream_t s)
 
 }  // namespace
 
-// 16 * Cols rows of 256 channels and two halves would take more than a lane's 512 registers.
-int attend_rows(int head_dim, int dtype, int64_t rows)
+int attend_rows(int head_dim, int64_t rows)
 {
-    const int most = head_dim == 256 && dtype == SPLITZIP_KV4_FP16 ? 64 : 128;
-    return rows <= 16 ? 16 : rows <= 64 ? 64 : most;
+    return rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 || head_dim == 256 ? 128 : 256;
 }
 
 void launch_attend(const AttendArgs &a, int head_dim, int dtype, int tile_rows, hipStream_t s)

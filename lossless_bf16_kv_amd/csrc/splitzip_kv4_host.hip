@@ -112,7 +112,7 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
          int *tile_rows)
 {
     const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
-    *tile_rows = attend_rows(c->head_dim, q->dtype, rows);
+    *tile_rows = attend_rows(c->head_dim, rows);
     const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
     int64_t tiles = ceil_div(rows, *tile_rows);
     KV4_REQUIRE(pairs <= INT32_MAX / 4, "too many sequences and heads");
@@ -121,7 +121,7 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
     if (q->window > 0)
         tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
     const int64_t blocks = std::max<int64_t>(1, pairs * tiles);
-    const int64_t splits = std::min<int64_t>(ceil_div(tokens, 256), 1024 / blocks);
+    const int64_t splits = std::min<int64_t>(ceil_div(tokens, 256), (*tile_rows == 16 ? 1024 : 512) / blocks);
     a->tiles = (int32_t)tiles;
     a->splits = (int32_t)std::max<int64_t>(1, splits);
     return SPLITZIP_OK;

@@ -68,7 +68,7 @@ struct EvictArgs {
 
 void launch_append(const AppendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_read(const ReadArgs &a, int head_dim, int dtype, hipStream_t s);
-int attend_rows(int head_dim, int dtype, int64_t rows);   // rows of a workgroup for this many rows a sequence
+int attend_rows(int head_dim, int64_t rows);   // rows of a workgroup for this many rows a sequence
 void launch_attend(const AttendArgs &a, int head_dim, int dtype, int tile_rows, hipStream_t s);
 void launch_weigh(const AttendArgs &a, int head_dim, int dtype, int max_q, int max_len, hipStream_t s);
 void launch_evict(const EvictArgs &a, int head_dim, hipStream_t s);

@@ -13,6 +13,8 @@
 //     tokens 4 quad .. + 3 of each group for one query, and V's layout gives it, for the same
 //     four tokens, D / 16 adjacent channels; channel r * D / 16 + t is row r of result tile t.
 //     So probabilities never leave their lane and V needs no transposition through memory.
+// v_mfma_f32_32x32x16_bf16 (half = l / 32): A row and B column l % 32, terms 8 half .. + 7; result
+//   rows 8 i + 4 half .. + 3 (i < 4) of column l % 32.
 #pragma once
 
 #include "splitzip_kv4_internal.h"
@@ -50,6 +52,25 @@ __device__ __forceinline__ bf16x8 frag(uint32_t a, uint32_t b, uint32_t c, uint3
 __device__ __forceinline__ f32x4 mfma(bf16x8 a, bf16x8 b, f32x4 c)
 {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+__device__ __forceinline__ f32x16 mfma32(bf16x8 a, bf16x8 b, f32x16 c)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+
+__device__ __forceinline__ float half_max(float x)       // over lanes l and l ^ 32
+{
+    auto a = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+    return fmaxf(as_float(a[0]), as_float(a[1]));
+}
+
+__device__ __forceinline__ float half_sum(float x)
+{
+    auto a = __builtin_amdgcn_permlane32_swap(bits(x), bits(x), false, false);
+    return as_float(a[0]) + as_float(a[1]);
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -140,10 +161,11 @@ __device__ __forceinline__ KRaw<D> load_k(const Cache &c, int page, int head, in
     return k;
 }
 
+// quad: which four tokens of the group.
 template <int D>
-__device__ __forceinline__ VRaw<D> load_v(const Cache &c, int page, int head, int g, int lane)
+__device__ __forceinline__ VRaw<D> load_v(const Cache &c, int page, int head, int g, int lane, int quad)
 {
-    const int r = lane & 15, quad = lane >> 4;
+    const int r = lane & 15;
     const int64_t t = group_first(c, page, head, g);
     VRaw<D> v;
     load_words<D>(c.v_codes + t * (D / 2) + quad * (2 * D) + r * (D / 8), v.w);
@@ -198,18 +220,50 @@ __device__ __forceinline__ void v_half(const VRaw<D> &v, int p, uint2 &lo, uint2
     hi.y = __builtin_amdgcn_perm(d, c, 0x07060302);
 }
 
-// Whether one of the lane's four tokens has a scale past the format's finite ones.
+// A product of a V that is not finite with a probability of 0 is a NaN also for queries that do not
+// see it.  Where that may happen the values are taken out (no_nan), and the queries that do see one get
+// their NaN from poison.  A scale byte past 252 makes its 32 channels so.
 __device__ __forceinline__ bool v_bad(uint32_t s)
 {
     return (s & 0xff) > 252 || ((s >> 8) & 0xff) > 252 || ((s >> 16) & 0xff) > 252 || (s >> 24) > 252;
 }
 
-// bf16 pair: elements that are not finite to 0 in x, and to 1 in `is` (others 0).
-__device__ __forceinline__ void split_finite(uint32_t &x, uint32_t &is)
+template <int D>
+__device__ __forceinline__ void no_nan(VRaw<D> &v)
 {
-    const bool lo = (x & 0x7f80u) == 0x7f80u, hi = (x & 0x7f800000u) == 0x7f800000u;
-    is = (lo ? 0x3f80u : 0u) | (hi ? 0x3f800000u : 0u);
-    x &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (((v.s >> (8 * i)) & 0xff) <= 252)
+            continue;
+        v.s &= ~(0xffu << (8 * i));
+        if constexpr (D == 64) {
+            v.w[i >> 1] &= i & 1 ? 0xffffu : 0xffff0000u;
+        } else {
+#pragma unroll
+            for (int k = 0; k < D / 128; ++k)
+                v.w[i * (D / 128) + k] = 0;
+        }
+    }
+}
+
+// Bit b: the query sees a token of group g whose block b of V is not finite.
+template <int D>
+__device__ __forceinline__ uint32_t poison(const Cache &c, const Batch &b, int s, int head, int g, const Mask &mask, int query)
+{
+    const int page = g < 0 ? -1 : page_of(c, b, s, 16 * g);
+    if (page < 0)
+        return 0;
+    const int64_t t0 = group_first(c, page, head, g), page0 = t0 >> c.page_shift << c.page_shift;
+    uint32_t bits = 0;
+#pragma unroll 1
+    for (int t = 0; t < 16; ++t) {
+        if (!mask.sees(query, 16 * g + t))
+            continue;
+#pragma unroll 1
+        for (int k = 0; k < D / 32; ++k)
+            bits |= (c.v_scales[page0 * (D / 32) + ((int64_t)k << c.page_shift) + (t0 - page0) + t] > 252 ? 1u : 0u) << k;
+    }
+    return bits;
 }
 
 // Eight channels of a query as bf16 (Half 0: the leading bits, 1: what an fp16 value has beyond
