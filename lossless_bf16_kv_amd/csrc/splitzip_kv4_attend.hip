@@ -116,11 +116,13 @@ struct Pair {
     int ga, gb;          // groups; -1: none, or on a bad page
 };
 
-template <int D, int T>
+// 16 * Cols rows a workgroup.
+template <int D, int T, int Cols>
 __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs a)
 {
     constexpr int kHalves = T == SPLITZIP_KV4_FP16 ? 2 : 1;
     constexpr int kSteps = D / 32, kTiles = D / 16;
+    constexpr int kRows = 16 * Cols;
     constexpr int kPitch = D + 4;
     __shared__ float sh_o[4][16][kPitch];
     __shared__ float sh_m[4][16], sh_l[4][16];
@@ -132,39 +134,54 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
     const Seq q = sequence(a.c, a.b, at.s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
+    // scores are scaled by |scale|: a negative one is in the queries' signs
+    const float scale = fabsf(a.scale2);
+    const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;
 
-    for (int row0 = at.tile * 16; row0 < rows; row0 += a.tiles * 16) {
+    for (int row0 = at.tile * kRows; row0 < rows; row0 += a.tiles * kRows) {
         const int base = q.len - q.n;
-        const int row = min(row0 + r, rows - 1);
-        const int query = base + row / a.group;
-        const int q_lo = base + row0 / a.group, q_hi = base + min(row0 + 15, rows - 1) / a.group;
-        const int64_t q_row = q.row0 + row / a.group;
-        const int q_head = at.head * a.group + row % a.group;
-        bf16x8 qf[kHalves][kSteps];
+        const int q_lo = base + row0 / a.group, q_hi = base + min(row0 + kRows - 1, rows - 1) / a.group;
+        int query[Cols];
+        bf16x8 qf[Cols][kHalves][kSteps];
 #pragma unroll
-        for (int st = 0; st < kSteps; ++st) {
-            const int64_t p = q_row * a.q_token + q_head * a.q_head + quad * (D / 4) + 8 * st;
-            qf[0][st] = q_frag<T, 0>(a.q, p, a.wide);
-            if constexpr (kHalves == 2)
-                qf[1][st] = q_frag<T, 1>(a.q, p, a.wide);
+        for (int c = 0; c < Cols; ++c) {
+            const int row = min(row0 + 16 * c + r, rows - 1);
+            query[c] = base + row / a.group;
+            const int64_t p = (q.row0 + row / a.group) * a.q_token + (at.head * a.group + row % a.group) * a.q_head +
+                              quad * (D / 4);
+#pragma unroll
+            for (int st = 0; st < kSteps; ++st) {
+                qf[c][0][st] = flip_sign(q_frag<T, 0>(a.q, p + 8 * st, a.wide), flip);
+                if constexpr (kHalves == 2)
+                    qf[c][1][st] = flip_sign(q_frag<T, 1>(a.q, p + 8 * st, a.wide), flip);
+            }
         }
         const Groups groups(q_lo, q_hi, a.window, a.sinks);
         int first, last;
         share(groups.count, a.splits, at.split, 8, first, last);
 
-        float m = -INFINITY, l = 0.0f;
-        uint32_t lost = 0;                       // blocks whose result is a NaN
-        f32x4 o[kTiles];
+        float m[Cols], l[Cols];
+        uint32_t lost[Cols];                     // blocks whose result is a NaN
+        f32x4 o[Cols][kTiles];
 #pragma unroll
-        for (int t = 0; t < kTiles; ++t)
-            o[t] = f32x4{0, 0, 0, 0};
+        for (int c = 0; c < Cols; ++c) {
+            m[c] = -INFINITY;
+            l[c] = 0.0f;
+            lost[c] = 0;
+#pragma unroll
+            for (int t = 0; t < kTiles; ++t)
+                o[c][t] = f32x4{0, 0, 0, 0};
+        }
 
-        auto fetch = [&](int v) {
+        Pages pages_a, pages_b;
+        const int v0 = first + 2 * wave;
+        auto fetch = [&](int i) {
             Pair<D> p;
+            const int v = v0 + 8 * i;
+            const int pa = pages_a.at(a.c, a.b, at.s, groups, v0, 8, last, i);
+            const int pb = pages_b.at(a.c, a.b, at.s, groups, v0 + 1, 8, last, i);
             p.ga = v < last ? groups.at(v) : -1;
             p.gb = v + 1 < last ? groups.at(v + 1) : -1;
-            const int pa = p.ga < 0 ? -1 : page_of(a.c, a.b, at.s, 16 * p.ga);
-            const int pb = p.gb < 0 ? -1 : page_of(a.c, a.b, at.s, 16 * p.gb);
             p.ka = load_k<D>(a.c, pa, at.head, p.ga, lane);
             p.kb = load_k<D>(a.c, pb, at.head, p.gb, lane);
             p.va = load_v<D>(a.c, pa, at.head, p.ga, lane, quad);
@@ -173,67 +190,79 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
             p.gb = pb < 0 ? -1 : p.gb;
             return p;
         };
-        int v = first + 2 * wave;
         Pair<D> next;
-        if (v < last)
-            next = fetch(v);
-        for (; v < last; v += 8) {
+        if (v0 < last)
+            next = fetch(0);
+        for (int n = 0; v0 + 8 * n < last; ++n) {
             Pair<D> cur = next;
-            if (v + 8 < last)
-                next = fetch(v + 8);
-            f32x4 sa = {0, 0, 0, 0}, sb = {0, 0, 0, 0};
+            if (v0 + 8 * n + 8 < last)
+                next = fetch(n + 1);
+            f32x4 sa[Cols], sb[Cols];
+#pragma unroll
+            for (int c = 0; c < Cols; ++c)
+                sa[c] = sb[c] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
                 const bf16x8 fa = k_frag<D>(cur.ka, st), fb = k_frag<D>(cur.kb, st);
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    sa = mfma(fa, qf[h][st], sa);
-                    sb = mfma(fb, qf[h][st], sb);
-                }
+                for (int c = 0; c < Cols; ++c)
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        sa[c] = mfma(fa, qf[c][h][st], sa[c]);
+                        sb[c] = mfma(fb, qf[c][h][st], sb[c]);
+                    }
             }
             const bool whole = cur.ga >= 0 && cur.gb >= 0 && mask.all(cur.ga, q_lo, q_hi) && mask.all(cur.gb, q_lo, q_hi);
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                x[i] = sa[i] * a.scale2;
-                x[4 + i] = sb[i] * a.scale2;
-            }
             const int ja = 16 * cur.ga + 4 * quad, jb = 16 * cur.gb + 4 * quad;
-            if (!whole) {
+            bf16x8 pf[Cols][kHalves];
+#pragma unroll
+            for (int c = 0; c < Cols; ++c) {
+                float x[8];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    x[i] = cur.ga >= 0 && mask.sees(query, ja + i) ? x[i] : -INFINITY;
-                    x[4 + i] = cur.gb >= 0 && mask.sees(query, jb + i) ? x[4 + i] : -INFINITY;
+                    x[i] = sa[c][i];
+                    x[4 + i] = sb[c][i];
                 }
-            }
-            float top = x[0];
+                if (!whole) {
 #pragma unroll
-            for (int i = 1; i < 8; ++i)
-                top = fmaxf(top, x[i]);
-            top = quad_max(top);
-            if (__any(top > m + 8.0f)) {
-                const float grown = fmaxf(m, top);
-                const float f = grown == -INFINITY ? 1.0f : exp2_fast(m - grown);
-                m = grown;
-                l *= f;
+                    for (int i = 0; i < 4; ++i) {
+                        x[i] = cur.ga >= 0 && mask.sees(query[c], ja + i) ? x[i] : -INFINITY;
+                        x[4 + i] = cur.gb >= 0 && mask.sees(query[c], jb + i) ? x[4 + i] : -INFINITY;
+                    }
+                }
+                float top = x[0];
 #pragma unroll
-                for (int t = 0; t < kTiles; ++t)
-                    o[t] *= f;
-            }
-            const float ref = m == -INFINITY ? 0.0f : m;
-            float p[8];
+                for (int i = 1; i < 8; ++i)
+                    top = fmaxf(top, x[i]);
+                top = quad_max(top) * scale;
+                if (__any(top > m[c] + 8.0f)) {
+                    const float grown = fmaxf(m[c], top);
+                    const float f = grown == -INFINITY ? 1.0f : exp2_fast(m[c] - grown);
+                    m[c] = grown;
+                    l[c] *= f;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = exp2_fast(x[i] - ref);
-                l += p[i];
+                    for (int t = 0; t < kTiles; ++t)
+                        o[c][t] *= f;
+                }
+                const float ref = m[c] == -INFINITY ? 0.0f : m[c];
+                float p[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    p[i] = exp2_fast(fmaf(x[i], scale, -ref));
+                    if (!whole)
+                        p[i] = x[i] == -INFINITY ? 0.0f : p[i];         // also where the scale is 0
+                    l[c] += p[i];
+                }
+                p_frag<kHalves>(p, pf[c]);
             }
-            bf16x8 pf[kHalves];
-            p_frag<kHalves>(p, pf);
             if (!whole && __any(v_bad(cur.va.s) || v_bad(cur.vb.s))) {
                 no_nan(cur.va);
                 no_nan(cur.vb);
-                lost |= poison<D>(a.c, a.b, at.s, at.head, cur.ga, mask, query);
-                lost |= poison<D>(a.c, a.b, at.s, at.head, cur.gb, mask, query);
+#pragma unroll
+                for (int c = 0; c < Cols; ++c) {
+                    lost[c] |= poison<D>(a.c, a.b, at.s, at.head, cur.ga, mask, query[c]);
+                    lost[c] |= poison<D>(a.c, a.b, at.s, at.head, cur.gb, mask, query[c]);
+                }
             }
 #pragma unroll
             for (int t = 0; t < kTiles; t += 2) {
@@ -242,79 +271,84 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
                 v_half<D>(cur.vb, t / 2, b0, b1);
                 const bf16x8 f0 = frag(a0.x, a0.y, b0.x, b0.y), f1 = frag(a1.x, a1.y, b1.x, b1.y);
 #pragma unroll
-                for (int h = 0; h < kHalves; ++h) {
-                    o[t] = mfma(f0, pf[h], o[t]);
-                    o[t + 1] = mfma(f1, pf[h], o[t + 1]);
-                }
+                for (int c = 0; c < Cols; ++c)
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h) {
+                        o[c][t] = mfma(f0, pf[c][h], o[c][t]);
+                        o[c][t + 1] = mfma(f1, pf[c][h], o[c][t + 1]);
+                    }
             }
-        }
-        if (__any(lost != 0)) {
-            // the lane's channels (4 quad + i) * kTiles + t: of block (4 quad + i) / 2
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (lost >> ((4 * quad + i) * kTiles / 32) & 1)
-#pragma unroll
-                    for (int t = 0; t < kTiles; ++t)
-                        o[t][i] = NAN;
         }
 
         // join the four waves
-        l = quad_sum(l);
-        if (quad == 0) {
-            sh_m[wave][r] = m;
-            sh_l[wave][r] = l;
-        }
-        // channels (4 quad + i) * kTiles + t of row r
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int c = 0; c < Cols; ++c) {
+            if (__any(lost[c] != 0)) {
+                // the lane's channels (4 quad + i) * kTiles + t: of block (4 quad + i) / 2
 #pragma unroll
-            for (int t = 0; t < kTiles; t += 4) {
-                const f32x4 x = {o[t][i], o[t + 1][i], o[t + 2][i], o[t + 3][i]};
-                *(f32x4 *)&sh_o[wave][r][(4 * quad + i) * kTiles + t] = x;
+                for (int i = 0; i < 4; ++i)
+                    if (lost[c] >> ((4 * quad + i) * kTiles / 32) & 1)
+#pragma unroll
+                        for (int t = 0; t < kTiles; ++t)
+                            o[c][t][i] = NAN;
             }
-        __syncthreads();
-        const int orow = threadIdx.x >> 4, part = threadIdx.x & 15;
-        float big = sh_m[0][orow];
+            l[c] = quad_sum(l[c]);
+            if (quad == 0) {
+                sh_m[wave][r] = m[c];
+                sh_l[wave][r] = l[c];
+            }
+            // channels (4 quad + i) * kTiles + t of row r
 #pragma unroll
-        for (int w = 1; w < 4; ++w)
-            big = fmaxf(big, sh_m[w][orow]);
-        float f[4], sum = 0.0f;
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-            f[w] = big == -INFINITY ? 1.0f : exp2_fast(sh_m[w][orow] - big);
-            sum += sh_l[w][orow] * f[w];
-        }
-        if (row0 + orow < rows) {
-            const int64_t g = (q.row0 + (row0 + orow) / a.group) * (int64_t)a.q_heads + at.head * a.group +
-                              (row0 + orow) % a.group;
-            // thread's channels: 4 part + 64 k
-            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+                for (int t = 0; t < kTiles; t += 4) {
+                    const f32x4 x = {o[c][t][i], o[c][t + 1][i], o[c][t + 2][i], o[c][t + 3][i]};
+                    *(f32x4 *)&sh_o[wave][r][(4 * quad + i) * kTiles + t] = x;
+                }
+            __syncthreads();
+            const int orow = threadIdx.x >> 4, part = threadIdx.x & 15;
+            const int row = row0 + 16 * c + orow;
+            float big = sh_m[0][orow];
 #pragma unroll
-            for (int k = 0; k < D; k += 64) {
-                const int d = k + 4 * part;
-                f32x4 x = *(const f32x4 *)&sh_o[0][orow][d] * f[0];
+            for (int w = 1; w < 4; ++w)
+                big = fmaxf(big, sh_m[w][orow]);
+            float f[4], sum = 0.0f;
 #pragma unroll
-                for (int w = 1; w < 4; ++w)
-                    x += *(const f32x4 *)&sh_o[w][orow][d] * f[w];
-                if (a.splits == 1) {
-                    x *= inv;
-                    *(uint2 *)((uint16_t *)a.out + g * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
-                } else {
-                    *(f32x4 *)(a.part_o + ((int64_t)at.split * a.b.total * a.q_heads + g) * D + d) = x;
+            for (int w = 0; w < 4; ++w) {
+                f[w] = big == -INFINITY ? 1.0f : exp2_fast(sh_m[w][orow] - big);
+                sum += sh_l[w][orow] * f[w];
+            }
+            if (row < rows) {
+                const int64_t g = (q.row0 + row / a.group) * (int64_t)a.q_heads + at.head * a.group + row % a.group;
+                // thread's channels: 4 part + 64 k
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+                for (int k = 0; k < D; k += 64) {
+                    const int d = k + 4 * part;
+                    f32x4 x = *(const f32x4 *)&sh_o[0][orow][d] * f[0];
+#pragma unroll
+                    for (int w = 1; w < 4; ++w)
+                        x += *(const f32x4 *)&sh_o[w][orow][d] * f[w];
+                    if (a.splits == 1) {
+                        x *= inv;
+                        *(uint2 *)((uint16_t *)a.out + g * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
+                    } else {
+                        *(f32x4 *)(a.part_o + ((int64_t)at.split * a.b.total * a.q_heads + g) * D + d) = x;
+                    }
+                }
+                if (part == 0) {
+                    if (a.splits == 1) {
+                        if (a.lse)
+                            a.lse[g] = sum == 0.0f ? -INFINITY : (big + __log2f(sum)) * kLn2;
+                    } else {
+                        float *ml = a.part_ml + ((int64_t)at.split * a.b.total * a.q_heads + g) * 2;
+                        ml[0] = big;
+                        ml[1] = sum;
+                    }
                 }
             }
-            if (part == 0) {
-                if (a.splits == 1) {
-                    if (a.lse)
-                        a.lse[g] = sum == 0.0f ? -INFINITY : (big + __log2f(sum)) * kLn2;
-                } else {
-                    float *ml = a.part_ml + ((int64_t)at.split * a.b.total * a.q_heads + g) * 2;
-                    ml[0] = big;
-                    ml[1] = sum;
-                }
-            }
+            __syncthreads();
         }
-        __syncthreads();
     }
 }
 
@@ -407,10 +441,12 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
         const int r = lane & 15, quad = lane >> 4;
         // the four tokens whose V a lane converts: lanes 0 .. 31 then write 256 adjacent bytes
         const int v_quad = 2 * (quad & 1) + (quad >> 1);
-        auto fetch = [&](int v) {
+        Pages pages;
+        auto fetch = [&](int i) {
             Raw x;
+            const int v = first + wave + kWaves * i;
+            const int page = pages.at(a.c, a.b, at.s, groups, first + wave, kWaves, last, i);
             x.g = v < last ? groups.at(v) : -1;
-            const int page = x.g < 0 ? -1 : page_of(a.c, a.b, at.s, 16 * x.g);
             x.k = load_k<D>(a.c, page, at.head, x.g, lane);
             x.v = load_v<D>(a.c, page, at.head, x.g, lane, v_quad);
             x.g = page < 0 ? -1 : x.g;
@@ -450,17 +486,16 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
         };
 
         if (first < last) {
-            raw = fetch(first + wave);
+            raw = fetch(0);
             put(raw, sh.stage[0]);
-            raw = fetch(first + kWaves + wave);
+            raw = fetch(1);
         }
         __syncthreads();
-        int buf = 0;
-        for (int v = first; v < last; v += kWaves, buf ^= 1) {
-            const Stage<D> &st = sh.stage[buf];
-            if (v + kWaves < last) {
-                put(raw, sh.stage[buf ^ 1]);
-                raw = fetch(v + 2 * kWaves + wave);
+        for (int i = 0; first + kWaves * i < last; ++i) {
+            const Stage<D> &st = sh.stage[i & 1];
+            if (first + kWaves * (i + 1) < last) {
+                put(raw, sh.stage[(i + 1) & 1]);
+                raw = fetch(i + 2);
             }
 #pragma unroll 1
             for (int tile = part; tile < kTiles; tile += kParts) {
@@ -621,29 +656,45 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
 
 // ---- joining splits -------------------------------------------------------------------------
 
-// D / 4 lanes a row: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, splits in order.
+// D / 4 lanes a row: o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s, splits in order.  The factors
+// are one a lane first, so that the loads of O do not wait for each other.
 template <int D, int T>
 __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
 {
+    constexpr int kRow = D / 4;
     const int64_t rows = a.b.total * a.q_heads;
-    const int64_t row = (int64_t)blockIdx.x * (kLanes / (D / 4)) + threadIdx.x / (D / 4);
-    const int d = threadIdx.x % (D / 4) * 4;
-    if (row >= rows)
-        return;
-    if (sequence_of(a.b, row / a.q_heads) < 0)
-        return;                                  // fill_unowned wrote it
+    const int64_t row = (int64_t)blockIdx.x * (kLanes / kRow) + threadIdx.x / kRow;
+    const int part = threadIdx.x % kRow, d = 4 * part;
+    // rows of no sequence: fill_unowned wrote them.  All lanes stay for the shuffles.
+    const bool mine = row < rows && sequence_of(a.b, row / a.q_heads) >= 0;
+    const int64_t from = row < rows ? row : 0;
     float big = -INFINITY;
-    for (int s = 0; s < a.splits; ++s)
-        big = fmaxf(big, a.part_ml[(s * rows + row) * 2]);
+    for (int s = part; s < a.splits; s += kRow)
+        big = fmaxf(big, a.part_ml[(s * rows + from) * 2]);
+#pragma unroll
+    for (int x = 1; x < kRow; x *= 2)
+        big = fmaxf(big, __shfl_xor(big, x));
     float sum = 0.0f;
     f32x4 x = {0, 0, 0, 0};
-    for (int s = 0; s < a.splits; ++s) {
-        const float m = a.part_ml[(s * rows + row) * 2], l = a.part_ml[(s * rows + row) * 2 + 1];
-        // m = -infinity: the split saw nothing, or NaN scores alone, which its sum holds
-        const float f = big == -INFINITY ? 1.0f : exp2_fast(m - big);
-        sum += l * f;
-        x += *(const f32x4 *)(a.part_o + (s * rows + row) * D + d) * f;
+    for (int s0 = 0; s0 < a.splits; s0 += kRow) {
+        const int s = s0 + part;
+        float f = 0.0f, l = 0.0f;
+        if (s < a.splits) {
+            const float m = a.part_ml[(s * rows + from) * 2];
+            // m = -infinity: the split saw nothing, or NaN scores alone, which its sum holds
+            f = big == -INFINITY ? 1.0f : exp2_fast(m - big);
+            l = a.part_ml[(s * rows + from) * 2 + 1] * f;
+        }
+        const int some = min(kRow, a.splits - s0);
+        for (int i = 0; i < some; ++i) {
+            const f32x4 y = *(const f32x4 *)(a.part_o + ((s0 + i) * rows + from) * D + d);
+            const float fi = __shfl(f, i, kRow);
+            sum += __shfl(l, i, kRow);
+            x += y * fi;
+        }
     }
+    if (!mine)
+        return;
     x *= sum == 0.0f ? 0.0f : 1.0f / sum;
     *(uint2 *)((uint16_t *)a.out + row * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
     if (d == 0 && a.lse)
@@ -656,8 +707,11 @@ void attend_dt(const AttendArgs &a, int tile_rows, hipStream_t s)
     const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.tiles * a.splits);
     constexpr int kLanesMany = 64 * Stage<D>::kWaves;
     if (tile_rows == 16)
-        few_rows<D, T><<<grid, kLanes, 0, s>>>(a);
-    else if (tile_rows == 64)
+        few_rows<D, T, 1><<<grid, kLanes, 0, s>>>(a);
+    else if (tile_rows == 32) {
+        if constexpr (D < 256)
+            few_rows<D, T, 2><<<grid, kLanes, 0, s>>>(a);
+    } else if (tile_rows == 64)
         many_rows<D, T, 2><<<grid, kLanesMany, 0, s>>>(a);
     else if (tile_rows == 128)
         many_rows<D, T, 4><<<grid, kLanesMany, 0, s>>>(a);
@@ -682,7 +736,7 @@ void attend_d(const AttendArgs &a, int dtype, int tile_rows, hipStream_t s)
 
 int attend_rows(int head_dim, int64_t rows)
 {
-    return rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 || head_dim == 256 ? 128 : 256;
+    return rows <= 16 ? 16 : rows <= 32 && head_dim < 256 ? 32 : rows <= 64 ? 64 : rows <= 128 || head_dim == 256 ? 128 : 256;
 }
 
 void launch_attend(const AttendArgs &a, int head_dim, int dtype, int tile_rows, hipStream_t s)

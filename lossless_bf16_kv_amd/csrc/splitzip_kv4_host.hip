@@ -121,7 +121,7 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
     if (q->window > 0)
         tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
     const int64_t blocks = std::max<int64_t>(1, pairs * tiles);
-    const int64_t splits = std::min<int64_t>(ceil_div(tokens, 256), (*tile_rows == 16 ? 1024 : 512) / blocks);
+    const int64_t splits = std::min<int64_t>(ceil_div(tokens, 256), (*tile_rows <= 32 ? 1024 : 512) / blocks);
     a->tiles = (int32_t)tiles;
     a->splits = (int32_t)std::max<int64_t>(1, splits);
     return SPLITZIP_OK;

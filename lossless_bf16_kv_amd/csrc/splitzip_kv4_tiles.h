@@ -94,6 +94,23 @@ struct Groups {
     __device__ int at(int v) const { return v < lead ? v : v + skip; }
 };
 
+// Pages of the groups first, first + step, .. of a wave, below `last`: 64 at a time, one a lane.  A page
+// looked up when its tokens are wanted would hold up the loads behind it by a load's time.
+struct Pages {
+    int list, from;              // lane i: page of step from + i
+    __device__ Pages() : list(-1), from(-64) {}
+    // Page of group first + i * step, or -1: none, or a bad page.  i grows by one from call to call.
+    __device__ int at(const Cache &c, const Batch &b, int s, const Groups &groups, int first, int step, int last, int i)
+    {
+        if (i >= from + 64) {
+            from = i;
+            const int64_t v = first + (int64_t)(i + (int)(threadIdx.x & 63)) * step;
+            list = v < last ? page_of(c, b, s, 16 * groups.at((int)v)) : -1;
+        }
+        return __builtin_amdgcn_readlane(list, i - from);
+    }
+};
+
 // Which tokens queries lo .. hi see.
 struct Mask {
     int window, sinks;
