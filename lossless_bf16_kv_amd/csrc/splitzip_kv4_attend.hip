@@ -131,7 +131,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, quad = lane >> 4;
     fill_unowned<D>(a, at);
-    const Seq q = sequence(a.c, a.b, at.s);
+    const Seq q = wave_sequence(a.c, a.b, at.s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
     // scores are scaled by |scale|: a negative one is in the queries' signs
@@ -392,7 +392,7 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
     const int m32 = lane & 31, half = lane >> 5;
     const int part = wave / Rows;
     fill_unowned<D>(a, at);
-    const Seq q = sequence(a.c, a.b, at.s);
+    const Seq q = wave_sequence(a.c, a.b, at.s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
     // scores are scaled by |scale|: a negative one is in the queries' signs

@@ -272,7 +272,7 @@ __global__ __launch_bounds__(kMove) void move_kernel(EvictArgs a)
     Batch bt = a.b;
     bt.cu = nullptr;
     const int64_t cap = (int64_t)a.out_width << a.c.page_shift;
-    const int keep = (int)min((int64_t)min(sequence(a.c, bt, s).len, a.budget), cap);
+    const int keep = (int)min((int64_t)min(wave_sequence(a.c, bt, s).len, a.budget), cap);
     const int to0 = turn * kTokens;
     if (to0 >= keep)
         return;

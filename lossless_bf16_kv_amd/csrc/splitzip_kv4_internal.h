@@ -144,6 +144,17 @@ __device__ __forceinline__ Seq sequence(const Cache &c, const Batch &b, int s)
     return q;
 }
 
+// The same for a sequence that a whole wave shares, in scalar registers: loads behind a store go to
+// vector ones, and every loop bound that follows from them would.
+__device__ __forceinline__ Seq wave_sequence(const Cache &c, const Batch &b, int s)
+{
+    Seq q = sequence(c, b, s);
+    q.len = __builtin_amdgcn_readfirstlane(q.len);
+    q.row0 = __builtin_amdgcn_readfirstlane(q.row0);
+    q.n = __builtin_amdgcn_readfirstlane(q.n);
+    return q;
+}
+
 // Sequence of row i, or -1: the last s with cu[s] <= i, if i < cu[s + 1].
 __device__ __forceinline__ int sequence_of(const Batch &b, int64_t i)
 {

@@ -161,34 +161,42 @@ __device__ __forceinline__ int64_t group_first(const Cache &c, int page, int hea
     return (((p * c.heads + head) << c.page_shift) | ((g << 4) & ((1 << c.page_shift) - 1)));
 }
 
+// Page and group are the wave's, so an address is a scalar base and a lane's 32-bit offset.  The empty
+// asm keeps the compiler from adding the offset to the buffer's start outside of the loop, which
+// would cost a 64-bit vector addition a load.
+__device__ __forceinline__ const uint8_t *lane_at(const uint8_t *base, uint32_t offset)
+{
+    asm volatile("" : "+v"(offset));
+    return base + offset;
+}
+
 template <int D>
 __device__ __forceinline__ KRaw<D> load_k(const Cache &c, int page, int head, int g, int lane)
 {
-    const int r = lane & 15, quad = lane >> 4;
-    const int64_t t = group_first(c, page, head, g) + r;
+    const uint32_t r = lane & 15, quad = lane >> 4;
+    const int64_t t = group_first(c, page, head, g);
     KRaw<D> k;
-    load_words<D>(c.k_codes + t * (D / 2) + quad * (D / 8), k.w);
+    load_words<D>(lane_at(c.k_codes + t * (D / 2), r * (D / 2) + quad * (D / 8)), k.w);
     const uint8_t *s = c.k_scales + t * (D / 32);
     if constexpr (D == 64)
-        k.s = s[quad >> 1];
+        k.s = *lane_at(s, r * 2 + (quad >> 1));
     else if constexpr (D == 128)
-        k.s = s[quad];
+        k.s = *lane_at(s, r * 4 + quad);
     else
-        k.s = *(const uint16_t *)(s + 2 * quad);
+        k.s = *(const uint16_t *)lane_at(s, r * 8 + 2 * quad);
     return k;
 }
 
 // quad: which four tokens of the group.
 template <int D>
-__device__ __forceinline__ VRaw<D> load_v(const Cache &c, int page, int head, int g, int lane, int quad)
+__device__ __forceinline__ VRaw<D> load_v(const Cache &c, int page, int head, int g, int lane, uint32_t quad)
 {
-    const int r = lane & 15;
-    const int64_t t = group_first(c, page, head, g);
+    const uint32_t r = lane & 15;
+    const int64_t t = group_first(c, page, head, g), page0 = t >> c.page_shift << c.page_shift;
     VRaw<D> v;
-    load_words<D>(c.v_codes + t * (D / 2) + quad * (2 * D) + r * (D / 8), v.w);
-    const int64_t page0 = t >> c.page_shift << c.page_shift;
-    const int in = (int)(t - page0) + 4 * quad;
-    v.s = *(const uint32_t *)(c.v_scales + page0 * (D / 32) + ((int64_t)(r * (D / 16) / 32) << c.page_shift) + in);
+    load_words<D>(lane_at(c.v_codes + t * (D / 2), quad * (2 * D) + r * (D / 8)), v.w);
+    const uint8_t *s = c.v_scales + page0 * (D / 32) + (t - page0);
+    v.s = *(const uint32_t *)lane_at(s, (r * (D / 16) / 32 << c.page_shift) + 4 * quad);
     return v;
 }
 

@@ -40,7 +40,7 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
     const int split = b % a.splits;
     b /= a.splits;
     const int head = b % a.c.heads, s = b / a.c.heads;
-    const Seq q = sequence(a.c, a.b, s);
+    const Seq q = wave_sequence(a.c, a.b, s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
     const int base = q.len - q.n;
@@ -114,7 +114,7 @@ __global__ __launch_bounds__(kLanes, D == 256 && NG == 4 ? 1 : 2) void rows_kern
     const int split = b % a.splits;
     b /= a.splits;
     const int head = b % a.c.heads, s = b / a.c.heads;
-    const Seq q = sequence(a.c, a.b, s);
+    const Seq q = wave_sequence(a.c, a.b, s);
     const int rows = q.n * a.group, base = q.len - q.n;
     const Mask mask = {a.window, a.sinks};
     const int all = rows > 0 ? (q.len + 15) >> 4 : 0;             // groups of the sequence
