@@ -8,26 +8,30 @@
 // rows of one token and a sum over rows stays in the lane but for one exchange at the end.
 //
 // step_kernel: up to 16 rows a sequence and KV head.  The rows' operands stay in registers while
-// a wave runs over groups of 16 tokens; HBM bounds it (K's 68 bytes a token at D = 128, and 8 of
-// weights).  rows_kernel: more rows.  A wave keeps the operands of its groups and the workgroup
-// runs over the rows through LDS; the matrix units and the exponentials bound it.
+// a wave runs over 64 tokens a turn, whose successors' codes and weights are on their way; HBM bounds
+// it (K's 68 bytes a token at D = 128, and 8 of weights).  rows_kernel: more rows.  A wave keeps the
+// operands of 64 tokens (32 at D = 256) and the workgroup runs over the rows through LDS; the matrix
+// unit and the exponentials bound it, at 8 cycles a wave's exponential about equally.
 #include "splitzip_kv4_tiles.h"
+
+#include <algorithm>
 
 namespace sz {
 namespace kv4 {
 namespace {
 
 constexpr int kLanes = 256;
+template <int D>
+constexpr int kWeighTokens = D == 256 ? 128 : 256;      // of a workgroup of rows_kernel
 
-// Adds the lane's sum for token 16 g + r of a page to its weight.
-__device__ __forceinline__ void add_weight(const Cache &c, int page, int head, int g, int len, int lane, float sum)
-{
-    sum = quad_sum(sum);
-    if (page < 0 || lane >= 16 || 16 * g + lane >= len)
-        return;
-    float *w = c.weights + group_first(c, page, head, g) + lane;
-    *w += sum;
-}
+// Groups of one turn of a wave, their K, and the weight of the lane's token 16 group[lane / 16] + lane % 16.
+template <int D>
+struct Turn {
+    KRaw<D> k[4];
+    int g[4], page[4];
+    float *at;               // null: no token
+    float w;
+};
 
 template <int D, int T>
 __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
@@ -48,8 +52,9 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
         return;
     // groups that some row sees; each wave keeps its own over all rows, 16 of which go at a time
     const Groups groups(base, q.len - 1, a.window, a.sinks);
-    const int per = (groups.count + a.splits - 1) / a.splits;
-    const int first = min(groups.count, split * per), last = min(groups.count, first + per);
+    const int per = ((groups.count + a.splits - 1) / a.splits + 15) & ~15;
+    const int first = min((int64_t)groups.count, (int64_t)split * per), last = min(groups.count, first + per);
+    const int turns = (last - first - 4 * wave + 15) >> 4;       // of this wave: 4 groups of every 16
     for (int row0 = 0; row0 < rows; row0 += 16) {
         const int row = min(row0 + r, rows - 1);
         const int64_t q_row = q.row0 + row / a.group;
@@ -74,42 +79,83 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
                                      : -INFINITY;
             lse[i] = t == -INFINITY ? INFINITY : t * kLog2e;      // adds 2^-infinity
         }
-        for (int v = first + wave; v < last; v += 4) {
-            const int g = groups.at(v);
-            const int page = page_of(a.c, a.b, s, 16 * g);
-            const KRaw<D> k = load_k<D>(a.c, page, head, g, lane);
-            f32x4 x = {0, 0, 0, 0};
-#pragma unroll
-            for (int st = 0; st < kSteps; ++st) {
-                const bf16x8 f = k_frag<D>(k, st);
-#pragma unroll
-                for (int h = 0; h < kHalves; ++h)
-                    x = mfma(qf[h][st], f, x);
+        const bool every = __all(lse[0] != INFINITY && lse[1] != INFINITY && lse[2] != INFINITY && lse[3] != INFINITY);
+
+        int list = -1, from = -16;       // pages of turns from .. + 15: lane 4 i + e has group e of turn i
+        auto fetch = [&](int i) {
+            if (i >= from + 16) {
+                from = i;
+                const int64_t v = first + 16 * (int64_t)(i + quad * 4 + r / 4) + 4 * wave + r % 4;
+                list = v < last ? page_of(a.c, a.b, s, 16 * groups.at((int)v)) : -1;
             }
-            const bool whole = mask.all(g, q_lo, q_hi);
-            float sum = 0.0f;
+            Turn<D> t;
+            int mine = -1, mine_g = 0;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float p = exp2_fast(fmaf(x[i], a.scale2, -lse[i]));
-                const bool in = lse[i] != INFINITY && (whole || mask.sees(query[i], 16 * g + r));
-                sum += in ? p : 0.0f;
+            for (int e = 0; e < 4; ++e) {
+                const int v = first + 16 * i + 4 * wave + e;
+                t.page[e] = __builtin_amdgcn_readlane(list, 4 * (i - from) + e);
+                t.g[e] = v < last ? groups.at(v) : -1;
+                t.k[e] = load_k<D>(a.c, t.page[e], head, t.g[e], lane);
+                mine = quad == e ? t.page[e] : mine;
+                mine_g = quad == e ? t.g[e] : mine_g;
             }
-            add_weight(a.c, page, head, g, q.len, lane, sum);
+            t.at = mine < 0 || 16 * mine_g + r >= q.len ? nullptr : a.c.weights + group_first(a.c, mine, head, mine_g) + r;
+            t.w = t.at ? *t.at : 0.0f;
+            return t;
+        };
+        Turn<D> next;
+        if (turns > 0)
+            next = fetch(0);
+        for (int i = 0; i < turns; ++i) {
+            const Turn<D> t = next;
+            if (i + 1 < turns)
+                next = fetch(i + 1);
+            float mine = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                f32x4 x = {0, 0, 0, 0};
+#pragma unroll
+                for (int st = 0; st < kSteps; ++st) {
+                    const bf16x8 f = k_frag<D>(t.k[e], st);
+#pragma unroll
+                    for (int h = 0; h < kHalves; ++h)
+                        x = mfma(qf[h][st], f, x);
+                }
+                float sum = 0.0f;
+                if (every && mask.all(t.g[e], q_lo, q_hi)) {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n)
+                        sum += exp2_fast(fmaf(x[n], a.scale2, -lse[n]));
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 4; ++n) {
+                        const float p = exp2_fast(fmaf(x[n], a.scale2, -lse[n]));
+                        sum += lse[n] != INFINITY && mask.sees(query[n], 16 * t.g[e] + r) ? p : 0.0f;
+                    }
+                }
+                sum = quad_sum(sum);
+                mine = quad == e ? sum : mine;
+            }
+            if (t.at)
+                *t.at = t.w + mine;
         }
     }
 }
 
-// NG groups of 16 tokens a wave; rows pass 32 at a time.
-template <int D, int T, int NG>
-__global__ __launch_bounds__(kLanes, D == 256 && NG == 4 ? 1 : 2) void rows_kernel(AttendArgs a)
+// Rows pass kBlock at a time, through two buffers in LDS: the loads of a block are on their way while
+// the block before is worked on.  Products have rows as their rows, so a sum over rows stays in a lane.
+template <int D, int T>
+__global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
 {
     constexpr int kHalves = T == SPLITZIP_KV4_FP16 ? 2 : 1;
-    constexpr int kSteps = D / 32;
-    constexpr int kBlock = 32;
-    __shared__ uint4 sh_q[2][kHalves][kBlock / 16][kSteps][64];
-    __shared__ float sh_lse[2][kBlock];
+    constexpr int kSteps = D / 16;
+    constexpr int kTiles = kWeighTokens<D> / 128;                // of 32 tokens, a wave
+    constexpr int kBlock = D * kHalves > 128 ? 32 : 64;
+    constexpr int kPieces = kBlock * (D / 8) / kLanes;           // 8 channels of a row, a lane
+    __shared__ uint4 sh_q[2][kHalves][kBlock / 32][kSteps][64];
+    __shared__ __align__(16) float sh_lse[2][kBlock / 32][2][16];    // in the order of a result's registers
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int r = lane & 15, quad = lane >> 4;
+    const int m32 = lane & 31, half = lane >> 5;
     uint32_t b = blockIdx.x;
     const int split = b % a.splits;
     b /= a.splits;
@@ -117,89 +163,139 @@ __global__ __launch_bounds__(kLanes, D == 256 && NG == 4 ? 1 : 2) void rows_kern
     const Seq q = wave_sequence(a.c, a.b, s);
     const int rows = q.n * a.group, base = q.len - q.n;
     const Mask mask = {a.window, a.sinks};
-    const int all = rows > 0 ? (q.len + 15) >> 4 : 0;             // groups of the sequence
+    const int len = rows > 0 ? q.len : 0;
 
-    for (int g0 = split * 4 * NG; g0 < all; g0 += a.splits * 4 * NG) {
-        const int j0 = 16 * g0, j1 = min(16 * (g0 + 4 * NG), q.len) - 1;     // the workgroup's tokens
+    for (int64_t j00 = (int64_t)split * kWeighTokens<D>; j00 < len; j00 += (int64_t)a.splits * kWeighTokens<D>) {
+        const int j0 = (int)j00, j1 = (int)min(j00 + kWeighTokens<D>, (int64_t)q.len) - 1;   // the workgroup's tokens
         // rows that see one of them: queries from j0, up to the window's end unless always visible
         const int64_t past = a.window > 0 && j0 >= a.sinks ? (int64_t)j1 + a.window - 1 : (int64_t)q.len;
         const int lo = max(0, j0 - base), hi = (int)min((int64_t)q.n - 1, past - base);
         if (lo > hi)
             continue;
         const int row_end = (hi + 1) * a.group;
-        int page[NG], group[NG];
-        bf16x8 kf[NG][kSteps];
-        float sum[NG];
+        // this wave's tokens; behind the last the last one again, whose sums are dropped
+        int page[kTiles], token[kTiles];
+        bf16x8 kf[kTiles][kSteps];
+        float sum[kTiles];
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-            group[n] = g0 + wave * NG + n;
-            page[n] = group[n] < all ? page_of(a.c, a.b, s, 16 * group[n]) : -1;
-            const KRaw<D> k = load_k<D>(a.c, page[n], head, group[n], lane);
+        for (int n = 0; n < kTiles; ++n) {
+            const int j = j0 + 32 * (wave * kTiles + n) + m32;
+            token[n] = min(j, q.len - 1);
+            page[n] = page_of(a.c, a.b, s, token[n]);
+            const int64_t at = group_first(a.c, page[n], head, token[n] >> 4) + (token[n] & 15);
+            uint32_t w[D / 16];
 #pragma unroll
-            for (int st = 0; st < kSteps; ++st)
-                kf[n][st] = k_frag<D>(k, st);
+            for (int i = 0; i < D / 64; ++i) {
+                const uint4 c = *(const uint4 *)(a.c.k_codes + at * (D / 2) + half * (D / 4) + 16 * i);
+                w[4 * i] = c.x; w[4 * i + 1] = c.y; w[4 * i + 2] = c.z; w[4 * i + 3] = c.w;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const float ks = scale_of(a.c.k_scales[at * (D / 32) + half * (D / 64) + i]);
+#pragma unroll
+                for (int st = 4 * i; st < 4 * i + 4; ++st)
+                    kf[n][st] = frag(dequant<0>(w[st], ks), dequant<1>(w[st], ks), dequant<2>(w[st], ks), dequant<3>(w[st], ks));
+            }
+            if (j >= q.len)
+                page[n] = -1;
             sum[n] = 0.0f;
         }
-        // 32 rows to LDS as operands: piece p of a row is channels 8 p .. + 7
-        auto stage = [&](int row0, int buf) {
+        // piece p of a row is channels 8 p .. + 7
+        struct Rows {
+            bf16x8 q[kPieces][kHalves];
+            float lse;
+        } next;
+        auto fetch = [&](int row0) {
+            Rows x;
 #pragma unroll
-            for (int i = threadIdx.x; i < kBlock * (D / 8); i += kLanes) {
-                const int y = i % kBlock, p = i / kBlock;
-                const int row = min(row0 + y, row_end - 1);
+            for (int i = 0; i < kPieces; ++i) {
+                const int row = min(row0 + (i * kLanes + (int)threadIdx.x) / (D / 8), row_end - 1), p = threadIdx.x % (D / 8);
                 const int64_t at = (q.row0 + row / a.group) * a.q_token + (head * a.group + row % a.group) * a.q_head + 8 * p;
-                const int to = (p / kSteps) * 16 + y % 16, st = p % kSteps;
-                sh_q[buf][0][y / 16][st][to] = __builtin_bit_cast(uint4, q_frag<T, 0>(a.q, at, a.wide));
+                x.q[i][0] = q_frag<T, 0>(a.q, at, a.wide);
                 if constexpr (kHalves == 2)
-                    sh_q[buf][1][y / 16][st][to] = __builtin_bit_cast(uint4, q_frag<T, 1>(a.q, at, a.wide));
+                    x.q[i][1] = q_frag<T, 1>(a.q, at, a.wide);
             }
-            if (threadIdx.x < kBlock) {
-                const int row = row0 + threadIdx.x;
-                const float t = row < row_end ? a.lse_in[(q.row0 + row / a.group) * (int64_t)a.q_heads + head * a.group + row % a.group]
-                                              : -INFINITY;
-                sh_lse[buf][threadIdx.x] = t == -INFINITY ? INFINITY : t * kLog2e;
-            }
+            x.lse = -INFINITY;
+            const int row = row0 + threadIdx.x;
+            if (threadIdx.x < kBlock && row < row_end)
+                x.lse = a.lse_in[(q.row0 + row / a.group) * (int64_t)a.q_heads + head * a.group + row % a.group];
+            return x;
         };
-        int buf = 0;
-        stage(lo * a.group, 0);
-        __syncthreads();
-        for (int row0 = lo * a.group; row0 < row_end; row0 += kBlock, buf ^= 1) {
-            if (row0 + kBlock < row_end)
-                stage(row0 + kBlock, buf ^ 1);
+        auto put = [&](const Rows &x, int buf) {
 #pragma unroll
-            for (int half = 0; half < kBlock / 16; ++half) {
-                const int y0 = row0 + 16 * half;
-                if (y0 >= row_end)
-                    break;
-                const int q_lo = base + y0 / a.group, q_hi = base + min(y0 + 15, row_end - 1) / a.group;
-                bf16x8 qf[kHalves][kSteps];
+            for (int i = 0; i < kPieces; ++i) {
+                const int y = (i * kLanes + threadIdx.x) / (D / 8), p = threadIdx.x % (D / 8);
+                const int to = p / kSteps * 32 + y % 32;
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
+                    sh_q[buf][h][y / 32][p % kSteps][to] = __builtin_bit_cast(uint4, x.q[i][h]);
+            }
+            if (threadIdx.x < kBlock) {
+                const int y = threadIdx.x % 32;
+                sh_lse[buf][threadIdx.x / 32][(y >> 2) & 1][(y >> 3) * 4 + (y & 3)] = x.lse == -INFINITY ? INFINITY : x.lse * kLog2e;
+            }
+        };
+        const int start = lo * a.group;
+        next = fetch(start);
+        put(next, 0);
+        if (start + kBlock < row_end)
+            next = fetch(start + kBlock);
+        __syncthreads();
+        int buf = 0;
+        for (int row0 = start; row0 < row_end; row0 += kBlock, buf ^= 1) {
+            if (row0 + kBlock < row_end) {
+                put(next, buf ^ 1);
+                if (row0 + 2 * kBlock < row_end)
+                    next = fetch(row0 + 2 * kBlock);
+            }
+#pragma unroll 1
+            for (int part = 0; part < kBlock / 32; ++part) {
+                const int y0 = row0 + 32 * part;
+                if (y0 >= row_end)
+                    break;
+                const int q_lo = base + y0 / a.group, q_hi = base + min(y0 + 31, row_end - 1) / a.group;
+                f32x16 x[kTiles];
 #pragma unroll
-                    for (int st = 0; st < kSteps; ++st)
-                        qf[h][st] = __builtin_bit_cast(bf16x8, sh_q[buf][h][half][st][lane]);
-                float lse[4];
+                for (int n = 0; n < kTiles; ++n)
+                    x[n] = f32x16{};
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    lse[i] = sh_lse[buf][16 * half + 4 * quad + i];
+                for (int st = 0; st < kSteps; ++st)
 #pragma unroll
-                for (int n = 0; n < NG; ++n) {
-                    f32x4 x = {0, 0, 0, 0};
+                    for (int h = 0; h < kHalves; ++h) {
+                        const bf16x8 f = __builtin_bit_cast(bf16x8, sh_q[buf][h][part][st][lane]);
 #pragma unroll
-                    for (int st = 0; st < kSteps; ++st)
+                        for (int n = 0; n < kTiles; ++n)
+                            x[n] = mfma32(f, kf[n][st], x[n]);
+                    }
+                float lse[16];
 #pragma unroll
-                        for (int h = 0; h < kHalves; ++h)
-                            x = mfma(qf[h][st], kf[n][st], x);
-                    if (mask.all(group[n], q_lo, q_hi) && __all(lse[0] != INFINITY && lse[1] != INFINITY &&
-                                                               lse[2] != INFINITY && lse[3] != INFINITY)) {
+                for (int e = 0; e < 16; e += 4) {
+                    const f32x4 t = *(const f32x4 *)&sh_lse[buf][part][half][e];
+                    lse[e] = t[0]; lse[e + 1] = t[1]; lse[e + 2] = t[2]; lse[e + 3] = t[3];
+                }
+                bool every = true;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            sum[n] += exp2_fast(fmaf(x[i], a.scale2, -lse[i]));
+                for (int e = 0; e < 16; ++e)
+                    every = every && lse[e] != INFINITY;
+                every = __all(every);
+#pragma unroll
+                for (int n = 0; n < kTiles; ++n) {
+                    const int g = (j0 >> 4) + 2 * (wave * kTiles + n);
+                    if (every && mask.all(g, q_lo, q_hi) && mask.all(g + 1, q_lo, q_hi)) {
+                        float other = 0.0f;
+#pragma unroll
+                        for (int e = 0; e < 16; e += 2) {
+                            sum[n] += exp2_fast(fmaf(x[n][e], a.scale2, -lse[e]));
+                            other += exp2_fast(fmaf(x[n][e + 1], a.scale2, -lse[e + 1]));
+                        }
+                        sum[n] += other;
                     } else {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int query = base + min(y0 + 4 * quad + i, row_end - 1) / a.group;
-                            const float p = exp2_fast(fmaf(x[i], a.scale2, -lse[i]));
-                            sum[n] += lse[i] != INFINITY && mask.sees(query, 16 * group[n] + r) ? p : 0.0f;
+                        for (int e = 0; e < 16; ++e) {
+                            const int y = y0 + 8 * (e >> 2) + 4 * half + (e & 3);
+                            const int query = base + min(y, row_end - 1) / a.group;
+                            const float p = exp2_fast(fmaf(x[n][e], a.scale2, -lse[e]));
+                            sum[n] += lse[e] != INFINITY && mask.sees(query, token[n]) ? p : 0.0f;
                         }
                     }
                 }
@@ -207,8 +303,13 @@ __global__ __launch_bounds__(kLanes, D == 256 && NG == 4 ? 1 : 2) void rows_kern
             __syncthreads();
         }
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
-            add_weight(a.c, page[n], head, group[n], q.len, lane, sum[n]);
+        for (int n = 0; n < kTiles; ++n) {
+            const float all = half_sum(sum[n]);
+            if (page[n] >= 0 && half == 0) {
+                float *w = a.c.weights + group_first(a.c, page[n], head, token[n] >> 4) + (token[n] & 15);
+                *w += all;
+            }
+        }
     }
 }
 
@@ -216,20 +317,16 @@ template <int D, int T>
 void weigh_dt(AttendArgs a, int max_q, int max_len, hipStream_t s)
 {
     const int64_t pairs = (int64_t)a.b.n_seqs * a.c.heads;
-    const int64_t groups = max_len / 16 + 1;
-    auto splits = [&](int64_t unit, int64_t most) {
-        const int64_t n = (groups + unit - 1) / unit;
-        return (int32_t)(n < most ? n : most);
-    };
     if ((int64_t)max_q * a.group <= 16) {
-        a.splits = splits(16, 1 << 20);
+        // 256 tokens a workgroup at least (one turn of each wave), and 4096 workgroups at most
+        const int64_t most = std::max<int64_t>(1, 4096 / pairs);
+        a.splits = (int32_t)std::min<int64_t>(most, max_len / 256 + 1);
         step_kernel<D, T><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
-    } else if (pairs * groups >= 16 * 512) {
-        a.splits = splits(16, 1 << 20);
-        rows_kernel<D, T, 4><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
     } else {
-        a.splits = splits(4, 1 << 20);
-        rows_kernel<D, T, 1><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
+        a.splits = max_len / kWeighTokens<D> + 1;
+        if (pairs * a.splits > INT32_MAX / 2)
+            a.splits = 1;
+        rows_kernel<D, T><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
     }
 }
 
