@@ -82,11 +82,38 @@ __device__ __forceinline__ void share(int count, int splits, int split, int unit
     last = min(count, first + per * unit);
 }
 
-__device__ __forceinline__ bf16x8 flip_sign(bf16x8 x, uint32_t flip)
+// Scores are scaled by a positive number: a negative scale's sign goes to the queries, and a scale of
+// 0 makes them 0.
+struct Scale {
+    float by;
+    uint32_t keep, flip;
+    __device__ explicit Scale(float s)
+    {
+        by = s == 0.0f ? 1.0f : fabsf(s);
+        keep = s == 0.0f ? 0u : 0xffffffffu;
+        flip = s < 0.0f ? 0x80008000u : 0u;
+    }
+    __device__ __forceinline__ bf16x8 operator()(bf16x8 x) const
+    {
+        uint4 w = __builtin_bit_cast(uint4, x);
+        w.x = (w.x & keep) ^ flip; w.y = (w.y & keep) ^ flip;
+        w.z = (w.z & keep) ^ flip; w.w = (w.w & keep) ^ flip;
+        return __builtin_bit_cast(bf16x8, w);
+    }
+};
+
+// Largest of N values.
+template <int N>
+__device__ __forceinline__ float max_of(const float (&x)[N])
 {
-    uint4 w = __builtin_bit_cast(uint4, x);
-    w.x ^= flip; w.y ^= flip; w.z ^= flip; w.w ^= flip;
-    return __builtin_bit_cast(bf16x8, w);
+    float a = x[0], b = x[1];
+#pragma unroll
+    for (int i = 2; i < N; i += 4) {
+        a = fmaxf(fmaxf(a, x[i]), x[i + 1]);
+        if (i + 3 < N)
+            b = fmaxf(fmaxf(b, x[i + 2]), x[i + 3]);
+    }
+    return fmaxf(a, b);
 }
 
 // Eight probabilities as an operand, in one or two halves.
@@ -134,9 +161,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
     const Seq q = wave_sequence(a.c, a.b, at.s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
-    // scores are scaled by |scale|: a negative one is in the queries' signs
-    const float scale = fabsf(a.scale2);
-    const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;
+    const Scale scale(a.scale2);
 
     for (int row0 = at.tile * kRows; row0 < rows; row0 += a.tiles * kRows) {
         const int base = q.len - q.n;
@@ -151,9 +176,9 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
                               quad * (D / 4);
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
-                qf[c][0][st] = flip_sign(q_frag<T, 0>(a.q, p + 8 * st, a.wide), flip);
+                qf[c][0][st] = scale(q_frag<T, 0>(a.q, p + 8 * st, a.wide));
                 if constexpr (kHalves == 2)
-                    qf[c][1][st] = flip_sign(q_frag<T, 1>(a.q, p + 8 * st, a.wide), flip);
+                    qf[c][1][st] = scale(q_frag<T, 1>(a.q, p + 8 * st, a.wide));
             }
         }
         const Groups groups(q_lo, q_hi, a.window, a.sinks);
@@ -230,11 +255,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
                         x[4 + i] = cur.gb >= 0 && mask.sees(query[c], jb + i) ? x[4 + i] : -INFINITY;
                     }
                 }
-                float top = x[0];
-#pragma unroll
-                for (int i = 1; i < 8; ++i)
-                    top = fmaxf(top, x[i]);
-                top = quad_max(top) * scale;
+                const float top = quad_max(max_of(x)) * scale.by;
                 if (__any(top > m[c] + 8.0f)) {
                     const float grown = fmaxf(m[c], top);
                     const float f = grown == -INFINITY ? 1.0f : exp2_fast(m[c] - grown);
@@ -248,9 +269,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
                 float p[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    p[i] = exp2_fast(fmaf(x[i], scale, -ref));
-                    if (!whole)
-                        p[i] = x[i] == -INFINITY ? 0.0f : p[i];         // also where the scale is 0
+                    p[i] = exp2_fast(fmaf(x[i], scale.by, -ref));
                     l[c] += p[i];
                 }
                 p_frag<kHalves>(p, pf[c]);
@@ -360,29 +379,29 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
 // which lanes read them, and every wave multiplies tiles of 32 tokens from there.  V's conversion
 // is shared, since it takes two instructions a value pair and a transposition; K's takes one, and its
 // codes are a quarter of the LDS traffic that bf16 would be.
-template <int D>
+template <int D, int kWaves>
 struct Stage {
-    static constexpr int kWaves = D == 256 ? 4 : 8;
     static constexpr int kTiles = kWaves / 2;            // of 32 tokens, a turn
     static constexpr int kLaneScales = D / 64;           // K's scale bytes of a lane: of D / 2 channels
     uint4 k[kTiles][D / 64][64];                         // lane (token l % 32): channels (l / 32) D / 2 ..
     uint4 v[kWaves][D / 32][64];                         // lane (channel): tokens 8 j + 4 (l / 32) .. + 3, j < 2
     uint8_t ks[kTiles][64][kLaneScales];
-    int group[kWaves];                                   // -1: none
-    int bad[kWaves];                                     // V of the group is not finite
+    int note[kWaves];                                    // of a group; 1: no page, 2: V is not finite
 };
 
-template <int D, int T, int Rows>
-__global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_rows(AttendArgs a)
+template <int D, int T, int kWaves, int Rows>
+__global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(AttendArgs a)
 {
     constexpr int kHalves = T == SPLITZIP_KV4_FP16 ? 2 : 1;
-    constexpr int kWaves = Stage<D>::kWaves, kTiles = Stage<D>::kTiles;
+    constexpr int kTiles = Stage<D, kWaves>::kTiles;
     constexpr int kSteps = D / 16, kOut = D / 32;
     constexpr int kParts = kWaves / Rows;                // waves that share rows
     constexpr int kRows = 32 * Rows;
     static_assert(kParts <= kTiles, "a wave without a tile");
+    // tiles worked on together: their products and exponentials do not wait for each other
+    constexpr int kJoin = D < 256 && kTiles / kParts >= 2 ? 2 : 1;
     __shared__ union Shared {
-        Stage<D> stage[2];
+        Stage<D, kWaves> stage[2];
         float join[kParts > 1 ? kWaves / 2 : 1][16 * kOut + 2][64];
         __device__ Shared() {}
     } sh;
@@ -395,9 +414,7 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
     const Seq q = wave_sequence(a.c, a.b, at.s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
-    // scores are scaled by |scale|: a negative one is in the queries' signs
-    const float scale = fabsf(a.scale2);
-    const uint32_t flip = a.scale2 < 0.0f ? 0x80008000u : 0u;
+    const Scale scale(a.scale2);
 
     // later rows see more tokens: they start first
     const int row_tiles = (rows + kRows - 1) / kRows;
@@ -418,9 +435,9 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
                                half * (D / 2);
 #pragma unroll
             for (int st = 0; st < kSteps; ++st) {
-                qf[0][st] = flip_sign(q_frag<T, 0>(a.q, p0 + 8 * st, a.wide), flip);
+                qf[0][st] = scale(q_frag<T, 0>(a.q, p0 + 8 * st, a.wide));
                 if constexpr (kHalves == 2)
-                    qf[1][st] = flip_sign(q_frag<T, 1>(a.q, p0 + 8 * st, a.wide), flip);
+                    qf[1][st] = scale(q_frag<T, 1>(a.q, p0 + 8 * st, a.wide));
             }
         }
         const int q_lo = base + min(w_row, rows - 1) / a.group;
@@ -452,7 +469,7 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
             x.g = page < 0 ? -1 : x.g;
             return x;
         };
-        auto put = [&](Raw &x, Stage<D> &st) {
+        auto put = [&](Raw &x, Stage<D, kWaves> &st) {
             const bool bad = __any(v_bad(x.v.s));
             if (bad)
                 no_nan(x.v);
@@ -479,10 +496,8 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
                 v[0] = lo;
                 v[32] = hi;                              // 16 lanes on
             }
-            if (lane == 0) {
-                st.bad[wave] = bad;
-                st.group[wave] = x.g;
-            }
+            if (lane == 0)
+                st.note[wave] = (x.g < 0 ? 1 : 0) | (bad ? 2 : 0);
         };
 
         if (first < last) {
@@ -492,56 +507,81 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
         }
         __syncthreads();
         for (int i = 0; first + kWaves * i < last; ++i) {
-            const Stage<D> &st = sh.stage[i & 1];
+            const Stage<D, kWaves> &st = sh.stage[i & 1];
             if (first + kWaves * (i + 1) < last) {
                 put(raw, sh.stage[(i + 1) & 1]);
                 raw = fetch(i + 2);
             }
+            int notes = 0;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                notes |= st.note[w];
+            notes = __builtin_amdgcn_readfirstlane(notes);
 #pragma unroll 1
-            for (int tile = part; tile < kTiles; tile += kParts) {
-                const int ga = __builtin_amdgcn_readfirstlane(st.group[2 * tile]);
-                const int gb = __builtin_amdgcn_readfirstlane(st.group[2 * tile + 1]);
-                if (!((ga >= 0 && 16 * ga <= q_hi) || (gb >= 0 && 16 * gb <= q_hi)))
-                    continue;
-                const bool whole = ga >= 0 && gb >= 0 && mask.all(ga, q_lo, q_hi) && mask.all(gb, q_lo, q_hi);
-                // scores of 32 tokens
-                f32x16 x = {};
-                {
-                    uint32_t s = 0;
+            for (int tile = part * kJoin; tile < kTiles; tile += kParts * kJoin) {
+                const int v = first + kWaves * i + 2 * tile;
+                if (v >= last || 16 * groups.at(v) > q_hi)
+                    break;
+                int g[2 * kJoin];                        // -1: none, or on a bad page
+                bool whole = true;
+#pragma unroll
+                for (int n = 0; n < 2 * kJoin; ++n) {
+                    g[n] = v + n < last ? groups.at(v + n) : -1;
+                    if (notes != 0 && (__builtin_amdgcn_readfirstlane(st.note[2 * tile + n]) & 1))
+                        g[n] = -1;
+                    whole = whole && g[n] >= 0 && mask.all(g[n], q_lo, q_hi);
+                }
+                // scores of 32 tokens a tile
+                f32x16 x[kJoin];
+                uint4 code[kJoin][D / 64];
+                uint32_t ks[kJoin];
+#pragma unroll
+                for (int n = 0; n < kJoin; ++n) {
+#pragma unroll
+                    for (int p = 0; p < D / 64; ++p)
+                        code[n][p] = st.k[tile + n][p][lane];
                     if constexpr (D == 64)
-                        s = st.ks[tile][lane][0];
+                        ks[n] = st.ks[tile + n][lane][0];
                     else if constexpr (D == 128)
-                        s = *(const uint16_t *)st.ks[tile][lane];
+                        ks[n] = *(const uint16_t *)st.ks[tile + n][lane];
                     else
-                        s = *(const uint32_t *)st.ks[tile][lane];
+                        ks[n] = *(const uint32_t *)st.ks[tile + n][lane];
+                    x[n] = f32x16{};
+                }
 #pragma unroll
-                    for (int p = 0; p < D / 64; ++p) {
-                        const uint4 c = st.k[tile][p][lane];
-                        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-                        const float ks = scale_of((s >> (8 * p)) & 0xff);       // 32 channels: one block
+                for (int p = 0; p < D / 64; ++p)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const bf16x8 f = frag(dequant<0>(w[i], ks), dequant<1>(w[i], ks), dequant<2>(w[i], ks),
-                                                  dequant<3>(w[i], ks));
+                    for (int e = 0; e < 4; ++e)
+#pragma unroll
+                        for (int n = 0; n < kJoin; ++n) {
+                            const uint4 c = code[n][p];
+                            const uint32_t w = e == 0 ? c.x : e == 1 ? c.y : e == 2 ? c.z : c.w;
+                            const float b = scale_of((ks[n] >> (8 * p)) & 0xff);       // 32 channels: one block
+                            const bf16x8 f = frag(dequant<0>(w, b), dequant<1>(w, b), dequant<2>(w, b), dequant<3>(w, b));
 #pragma unroll
                             for (int h = 0; h < kHalves; ++h)
-                                x = mfma32(f, qf[h][4 * p + i], x);
+                                x[n] = mfma32(f, qf[h][4 * p + e], x[n]);
                         }
-                    }
-                }
                 if (!whole) {
 #pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int g = e < 8 ? ga : gb;
-                        const int j = 16 * g + 8 * ((e >> 2) & 1) + 4 * half + (e & 3);
-                        x[e] = g >= 0 && mask.sees(query, j) ? x[e] : -INFINITY;
-                    }
-                }
-                float top = x[0];
+                    for (int n = 0; n < kJoin; ++n)
 #pragma unroll
-                for (int e = 1; e < 16; ++e)
-                    top = fmaxf(top, x[e]);
-                top = half_max(top) * scale;
+                        for (int e = 0; e < 16; ++e) {
+                            const int gr = g[2 * n + (e >> 3)];
+                            const int j = 16 * gr + 8 * ((e >> 2) & 1) + 4 * half + (e & 3);
+                            x[n][e] = gr >= 0 && mask.sees(query, j) ? x[n][e] : -INFINITY;
+                        }
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int n = 0; n < kJoin; ++n) {
+                    float y[16];
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        y[e] = x[n][e];
+                    top = fmaxf(top, max_of(y));
+                }
+                top = half_max(top) * scale.by;
                 if (__any(top > m + 8.0f)) {
                     const float grown = fmaxf(m, top);
                     const float f = grown == -INFINITY ? 1.0f : exp2_fast(m - grown);
@@ -552,31 +592,32 @@ __global__ __launch_bounds__(64 * Stage<D>::kWaves, D == 256 ? 1 : 2) void many_
                         o[t] *= f;
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
-                bf16x8 pf[2][kHalves];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    float p[8];
+                for (int n = 0; n < kJoin; ++n)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        p[e] = exp2_fast(fmaf(x[8 * h + e], scale, -ref));
-                        if (!whole)
-                            p[e] = x[8 * h + e] == -INFINITY ? 0.0f : p[e];     // also where the scale is 0
-                        l += p[e];
+                    for (int h = 0; h < 2; ++h) {
+                        float p[8], sum[2] = {0.0f, 0.0f};
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            p[e] = exp2_fast(fmaf(x[n][8 * h + e], scale.by, -ref));
+                            sum[e & 1] += p[e];
+                        }
+                        l += sum[0] + sum[1];
+                        bf16x8 pf[kHalves];
+                        p_frag<kHalves>(p, pf);
+#pragma unroll
+                        for (int t = 0; t < kOut; ++t) {
+                            const bf16x8 y = __builtin_bit_cast(bf16x8, st.v[2 * (tile + n) + h][t][lane]);
+#pragma unroll
+                            for (int k = 0; k < kHalves; ++k)
+                                o[t] = mfma32(y, pf[k], o[t]);
+                        }
                     }
-                    p_frag<kHalves>(p, pf[h]);
-                }
+                if (notes & 2) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int t = 0; t < kOut; ++t) {
-                        const bf16x8 y = __builtin_bit_cast(bf16x8, st.v[2 * tile + h][t][lane]);
-#pragma unroll
-                        for (int i = 0; i < kHalves; ++i)
-                            o[t] = mfma32(y, pf[h][i], o[t]);
-                    }
-                if (__builtin_amdgcn_readfirstlane(st.bad[2 * tile] | st.bad[2 * tile + 1])) {
-                    lost |= poison<D>(a.c, a.b, at.s, at.head, ga, mask, query);
-                    lost |= poison<D>(a.c, a.b, at.s, at.head, gb, mask, query);
+                    for (int n = 0; n < 2 * kJoin; ++n)
+                        if (__builtin_amdgcn_readfirstlane(st.note[2 * tile + n]) & 2)
+                            lost |= poison<D>(a.c, a.b, at.s, at.head, g[n], mask, query);
                 }
             }
             __syncthreads();
@@ -705,18 +746,18 @@ template <int D, int T>
 void attend_dt(const AttendArgs &a, int tile_rows, hipStream_t s)
 {
     const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.tiles * a.splits);
-    constexpr int kLanesMany = 64 * Stage<D>::kWaves;
+    constexpr int kWaves = D == 256 ? 4 : 8, kLanesMany = 64 * kWaves;
     if (tile_rows == 16)
         few_rows<D, T, 1><<<grid, kLanes, 0, s>>>(a);
     else if (tile_rows == 32) {
         if constexpr (D < 256)
             few_rows<D, T, 2><<<grid, kLanes, 0, s>>>(a);
     } else if (tile_rows == 64)
-        many_rows<D, T, 2><<<grid, kLanesMany, 0, s>>>(a);
+        many_rows<D, T, kWaves, 2><<<grid, kLanesMany, 0, s>>>(a);
     else if (tile_rows == 128)
-        many_rows<D, T, 4><<<grid, kLanesMany, 0, s>>>(a);
+        many_rows<D, T, kWaves, 4><<<grid, kLanesMany, 0, s>>>(a);
     else if constexpr (D < 256)
-        many_rows<D, T, 8><<<grid, kLanesMany, 0, s>>>(a);
+        many_rows<D, T, kWaves, 8><<<grid, kLanesMany, 0, s>>>(a);
     if (a.splits > 1) {
         constexpr int kRows = kLanes / (D / 4);
         join_kernel<D, T><<<(unsigned)((a.b.total * a.q_heads + kRows - 1) / kRows), kLanes, 0, s>>>(a);

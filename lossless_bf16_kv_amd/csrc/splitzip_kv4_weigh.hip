@@ -154,6 +154,7 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
     constexpr int kPieces = kBlock * (D / 8) / kLanes;           // 8 channels of a row, a lane
     __shared__ uint4 sh_q[2][kHalves][kBlock / 32][kSteps][64];
     __shared__ __align__(16) float sh_lse[2][kBlock / 32][2][16];    // in the order of a result's registers
+    __shared__ int sh_every[2][kBlock / 32];                     // all of these 32 rows count
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m32 = lane & 31, half = lane >> 5;
     uint32_t b = blockIdx.x;
@@ -200,7 +201,9 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
                 page[n] = -1;
             sum[n] = 0.0f;
         }
-        // piece p of a row is channels 8 p .. + 7
+        // Piece p of a row is channels 8 p .. + 7.  Lanes of one row write pieces 1 KiB apart, so rows are
+        // permuted among the 16 banks of 16 bytes, differently for each piece.
+        auto spread = [](int st, int part) { return (2 * st + part) & 15; };
         struct Rows {
             bf16x8 q[kPieces][kHalves];
             float lse;
@@ -225,13 +228,16 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const int y = (i * kLanes + threadIdx.x) / (D / 8), p = threadIdx.x % (D / 8);
-                const int to = p / kSteps * 32 + y % 32;
+                const int st = p % kSteps, to = p / kSteps * 32 + (y % 32 ^ spread(st, p / kSteps));
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h)
-                    sh_q[buf][h][y / 32][p % kSteps][to] = __builtin_bit_cast(uint4, x.q[i][h]);
+                    sh_q[buf][h][y / 32][st][to] = __builtin_bit_cast(uint4, x.q[i][h]);
             }
             if (threadIdx.x < kBlock) {
                 const int y = threadIdx.x % 32;
+                const uint64_t some = __ballot(x.lse != -INFINITY);
+                if (y == 0)
+                    sh_every[buf][threadIdx.x / 32] = (uint32_t)(some >> (lane & 32)) == 0xffffffffu;
                 sh_lse[buf][threadIdx.x / 32][(y >> 2) & 1][(y >> 3) * 4 + (y & 3)] = x.lse == -INFINITY ? INFINITY : x.lse * kLog2e;
             }
         };
@@ -258,26 +264,26 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n)
                     x[n] = f32x16{};
+                const bool every = __builtin_amdgcn_readfirstlane(sh_every[buf][part]) != 0;
 #pragma unroll
-                for (int st = 0; st < kSteps; ++st)
+                for (int h = 0; h < kHalves; ++h) {
+                    bf16x8 f[kSteps];
 #pragma unroll
-                    for (int h = 0; h < kHalves; ++h) {
-                        const bf16x8 f = __builtin_bit_cast(bf16x8, sh_q[buf][h][part][st][lane]);
+                    for (int st = 0; st < kSteps; ++st)
+                        f[st] = __builtin_bit_cast(bf16x8, sh_q[buf][h][part][st][half * 32 + (m32 ^ spread(st, half))]);
+                    __builtin_amdgcn_sched_barrier(0);           // all loads first
+#pragma unroll
+                    for (int st = 0; st < kSteps; ++st)
 #pragma unroll
                         for (int n = 0; n < kTiles; ++n)
-                            x[n] = mfma32(f, kf[n][st], x[n]);
-                    }
+                            x[n] = mfma32(f[st], kf[n][st], x[n]);
+                }
                 float lse[16];
 #pragma unroll
                 for (int e = 0; e < 16; e += 4) {
                     const f32x4 t = *(const f32x4 *)&sh_lse[buf][part][half][e];
                     lse[e] = t[0]; lse[e + 1] = t[1]; lse[e + 2] = t[2]; lse[e + 3] = t[3];
                 }
-                bool every = true;
-#pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    every = every && lse[e] != INFINITY;
-                every = __all(every);
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) {
                     const int g = (j0 >> 4) + 2 * (wave * kTiles + n);
