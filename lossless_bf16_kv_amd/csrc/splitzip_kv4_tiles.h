@@ -116,7 +116,7 @@ struct Mask {
     int window, sinks;
     __device__ bool sees(int query, int j) const
     {
-        return j <= query && (j < sinks || window == 0 || j > query - window);
+        return (j <= query) & ((j < sinks) | (window == 0) | (j > query - window));
     }
     // every query of lo .. hi sees every token of group g
     __device__ bool all(int g, int lo, int hi) const

@@ -21,6 +21,20 @@ namespace kv4 {
 namespace {
 
 constexpr int kLanes = 256;
+// Query and head of a row, moved on without a division.
+struct RowAt {
+    int query, head;
+    __device__ RowAt(int row, int group) : query(row / group), head(row % group) {}
+    __device__ __forceinline__ bool move(int queries, int heads, int group)      // heads < group
+    {
+        head += heads;
+        const bool over = head >= group;
+        head -= over ? group : 0;
+        query += queries + over;
+        return over;
+    }
+};
+
 template <int D>
 constexpr int kWeighTokens = D == 256 ? 128 : 256;      // of a workgroup of rows_kernel
 
@@ -154,6 +168,7 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
     constexpr int kPieces = kBlock * (D / 8) / kLanes;           // 8 channels of a row, a lane
     __shared__ uint4 sh_q[2][kHalves][kBlock / 32][kSteps][64];
     __shared__ __align__(16) float sh_lse[2][kBlock / 32][2][16];    // in the order of a result's registers
+    __shared__ __align__(16) int sh_query[2][kBlock / 32][2][16];
     __shared__ int sh_every[2][kBlock / 32];                     // all of these 32 rows count
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m32 = lane & 31, half = lane >> 5;
@@ -207,21 +222,42 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
         struct Rows {
             bf16x8 q[kPieces][kHalves];
             float lse;
+            int query;           // its token; a row behind the last has none, -1
         } next;
+        const int start = lo * a.group;
+        const int by_q = kBlock / a.group, by_f = kBlock % a.group;     // a block's step
+        const int64_t step = by_q * a.q_token + by_f * a.q_head, step_over = step + a.q_token - a.group * a.q_head;
+        int at_head[kPieces];
+        int64_t at[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) {
+            const RowAt x(start + (i * kLanes + (int)threadIdx.x) / (D / 8), a.group);
+            at_head[i] = x.head;
+            at[i] = (q.row0 + x.query) * a.q_token + (head * a.group + x.head) * a.q_head + 8 * (threadIdx.x % (D / 8));
+        }
+        RowAt lse_at(start + threadIdx.x % kBlock, a.group);
+        // each call is for the next block
         auto fetch = [&](int row0) {
             Rows x;
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const int row = min(row0 + (i * kLanes + (int)threadIdx.x) / (D / 8), row_end - 1), p = threadIdx.x % (D / 8);
-                const int64_t at = (q.row0 + row / a.group) * a.q_token + (head * a.group + row % a.group) * a.q_head + 8 * p;
-                x.q[i][0] = q_frag<T, 0>(a.q, at, a.wide);
+                const bool in = row0 + (i * kLanes + (int)threadIdx.x) / (D / 8) < row_end;
+                const int64_t p = in ? at[i] : q.row0 * a.q_token + head * a.group * a.q_head;
+                x.q[i][0] = q_frag<T, 0>(a.q, p, a.wide);
                 if constexpr (kHalves == 2)
-                    x.q[i][1] = q_frag<T, 1>(a.q, at, a.wide);
+                    x.q[i][1] = q_frag<T, 1>(a.q, p, a.wide);
+                at_head[i] += by_f;
+                const bool over = at_head[i] >= a.group;
+                at_head[i] -= over ? a.group : 0;
+                at[i] += over ? step_over : step;
             }
             x.lse = -INFINITY;
-            const int row = row0 + threadIdx.x;
-            if (threadIdx.x < kBlock && row < row_end)
-                x.lse = a.lse_in[(q.row0 + row / a.group) * (int64_t)a.q_heads + head * a.group + row % a.group];
+            x.query = -1;
+            if (threadIdx.x < kBlock && row0 + (int)threadIdx.x < row_end) {
+                x.query = base + lse_at.query;
+                x.lse = a.lse_in[(q.row0 + lse_at.query) * (int64_t)a.q_heads + head * a.group + lse_at.head];
+            }
+            lse_at.move(by_q, by_f, a.group);
             return x;
         };
         auto put = [&](const Rows &x, int buf) {
@@ -238,16 +274,19 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
                 const uint64_t some = __ballot(x.lse != -INFINITY);
                 if (y == 0)
                     sh_every[buf][threadIdx.x / 32] = (uint32_t)(some >> (lane & 32)) == 0xffffffffu;
-                sh_lse[buf][threadIdx.x / 32][(y >> 2) & 1][(y >> 3) * 4 + (y & 3)] = x.lse == -INFINITY ? INFINITY : x.lse * kLog2e;
+                const int to = (y >> 3) * 4 + (y & 3);
+                sh_lse[buf][threadIdx.x / 32][(y >> 2) & 1][to] = x.lse == -INFINITY ? INFINITY : x.lse * kLog2e;
+                sh_query[buf][threadIdx.x / 32][(y >> 2) & 1][to] = x.lse == -INFINITY ? -1 : x.query;
             }
         };
-        const int start = lo * a.group;
         next = fetch(start);
         put(next, 0);
         if (start + kBlock < row_end)
             next = fetch(start + kBlock);
         __syncthreads();
         int buf = 0;
+        RowAt first(start, a.group), last(start + 31, a.group);         // of 32 rows
+        const int by_q32 = 32 / a.group, by_f32 = 32 % a.group;
         for (int row0 = start; row0 < row_end; row0 += kBlock, buf ^= 1) {
             if (row0 + kBlock < row_end) {
                 put(next, buf ^ 1);
@@ -259,11 +298,15 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
                 const int y0 = row0 + 32 * part;
                 if (y0 >= row_end)
                     break;
-                const int q_lo = base + y0 / a.group, q_hi = base + min(y0 + 31, row_end - 1) / a.group;
+                const int q_lo = base + first.query, q_hi = base + min(last.query, hi);
+                first.move(by_q32, by_f32, a.group);
+                last.move(by_q32, by_f32, a.group);
                 f32x16 x[kTiles];
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n)
                     x[n] = f32x16{};
+                if (16 * ((j0 >> 4) + 2 * wave * kTiles) > q_hi)
+                    continue;                                    // none of the wave's tokens
                 const bool every = __builtin_amdgcn_readfirstlane(sh_every[buf][part]) != 0;
 #pragma unroll
                 for (int h = 0; h < kHalves; ++h) {
@@ -287,23 +330,20 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
 #pragma unroll
                 for (int n = 0; n < kTiles; ++n) {
                     const int g = (j0 >> 4) + 2 * (wave * kTiles + n);
+                    float part_sum[2] = {0.0f, 0.0f};
                     if (every && mask.all(g, q_lo, q_hi) && mask.all(g + 1, q_lo, q_hi)) {
-                        float other = 0.0f;
 #pragma unroll
-                        for (int e = 0; e < 16; e += 2) {
-                            sum[n] += exp2_fast(fmaf(x[n][e], a.scale2, -lse[e]));
-                            other += exp2_fast(fmaf(x[n][e + 1], a.scale2, -lse[e + 1]));
-                        }
-                        sum[n] += other;
-                    } else {
+                        for (int e = 0; e < 16; ++e)
+                            part_sum[e & 1] += exp2_fast(fmaf(x[n][e], a.scale2, -lse[e]));
+                    } else if (16 * g <= q_hi) {
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int y = y0 + 8 * (e >> 2) + 4 * half + (e & 3);
-                            const int query = base + min(y, row_end - 1) / a.group;
+                            const int query = sh_query[buf][part][half][e];
                             const float p = exp2_fast(fmaf(x[n][e], a.scale2, -lse[e]));
-                            sum[n] += lse[e] != INFINITY && mask.sees(query, token[n]) ? p : 0.0f;
+                            part_sum[e & 1] += mask.sees(query, token[n]) ? p : 0.0f;
                         }
                     }
+                    sum[n] += part_sum[0] + part_sum[1];
                 }
             }
             __syncthreads();
