@@ -709,6 +709,14 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
     // rows of no sequence: fill_unowned wrote them.  All lanes stay for the shuffles.
     const bool mine = row < rows && sequence_of(a.b, row / a.q_heads) >= 0;
     const int64_t from = row < rows ? row : 0;
+    // O of eight splits at a time, the first on their way before the factors are known
+    f32x4 y[8];
+    auto load = [&](int s) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            y[e] = *(const f32x4 *)(a.part_o + (min(s + e, a.splits - 1) * rows + from) * D + d);
+    };
+    load(0);
     float big = -INFINITY;
     for (int s = part; s < a.splits; s += kRow)
         big = fmaxf(big, a.part_ml[(s * rows + from) * 2]);
@@ -726,12 +734,16 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
             f = big == -INFINITY ? 1.0f : exp2_fast(m - big);
             l = a.part_ml[(s * rows + from) * 2 + 1] * f;
         }
-        const int some = min(kRow, a.splits - s0);
-        for (int i = 0; i < some; ++i) {
-            const f32x4 y = *(const f32x4 *)(a.part_o + ((s0 + i) * rows + from) * D + d);
-            const float fi = __shfl(f, i, kRow);
-            sum += __shfl(l, i, kRow);
-            x += y * fi;
+        for (int i = 0; i < kRow && s0 + i < a.splits; i += 8) {
+            if (s0 + i > 0)
+                load(s0 + i);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float fe = __shfl(f, i + e, kRow);
+                sum += __shfl(l, i + e, kRow);
+                if (s0 + i + e < a.splits)
+                    x += y[e] * fe;
+            }
         }
     }
     if (!mine)

@@ -26,6 +26,7 @@ import ctypes
 from . import E_DEVICE, SplitZipError, _check, lib
 
 BAD_PAGE, BAD_LENGTH, BAD_OFFSETS = 1, 2, 4     # bits of the status word
+_BIG = (1 << 31) - 1
 BLOCK = 32                                      # channels that share a scale
 
 
@@ -138,6 +139,10 @@ class KV4Cache:
         self._ref = ctypes.byref(self._c)
         self._L = _lib()
         self._dtypes = _dtypes()
+        self._index = k.device.index or 0
+        self._stream = torch._C._cuda_getCurrentRawStream       # calls of a few microseconds: no lookups in them
+        self._i32, self._f32 = torch.int32, torch.float32
+        self._empty, self._empty_like = torch.empty, torch.empty_like
 
     @property
     def page_bytes(self) -> int:
@@ -146,12 +151,11 @@ class KV4Cache:
 
     # -- arguments --------------------------------------------------------------------------
     def _int32(self, t, name: str, shape=None):
-        import torch
-        if t.dtype != torch.int32 or t.device != self.device:
+        if t.dtype is not self._i32 or t.device != self.device:
             raise ValueError(f"{name} must be int32 on {self.device}, got {t.dtype} on {t.device}")
-        if shape is not None and tuple(t.shape) != shape:
+        if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
-        if t.dim() and t.shape[-1] > 1 and t.stride(-1) != 1:
+        if t.stride(-1) != 1 and t.shape[-1] > 1:
             raise ValueError(f"{name} must be contiguous along its last dimension")
         return t.data_ptr()
 
@@ -159,9 +163,10 @@ class KV4Cache:
         if table.dim() != 2:
             raise ValueError("table must be [seqs, pages]")
         n, width = table.shape
+        if max_len is None:
+            max_len = width * self.page_size
         b = splitzip_kv4_batch(self._int32(table, "table"), self._int32(lens, "lens", (n,)), None,
-                               table.stride(0), total, width, n, 1,
-                               min(width * self.page_size if max_len is None else max_len, (1 << 31) - 1))
+                               table.stride(0), total, width, n, 1, max_len if max_len < _BIG else _BIG)
         if cu is not None:
             b.cu_seqlens = self._int32(cu, "cu", (n + 1,))
             b.max_q = total if max_q is None else max_q
@@ -174,7 +179,8 @@ class KV4Cache:
         code = self._dtypes.get(t.dtype, types)
         if code >= types:
             raise TypeError(f"{name} must be {', '.join(str(d) for d, c in self._dtypes.items() if c < types)}, got {t.dtype}")
-        if t.dim() != 3 or t.shape[2] != self.head_dim or (heads is not None and t.shape[1] != heads):
+        shape = t.shape
+        if len(shape) != 3 or shape[2] != self.head_dim or (heads is not None and shape[1] != heads):
             raise ValueError(f"{name} must be [rows, {heads or 'heads'}, {self.head_dim}], got {tuple(t.shape)}")
         if t.device != self.device:
             raise ValueError(f"{name} is on {t.device}, the cache is on {self.device}")
@@ -188,13 +194,13 @@ class KV4Cache:
             raise ValueError("window must be at least 1 (None: no window)")
         if sinks < 0:
             raise ValueError("sinks must not be negative")
-        big = (1 << 31) - 1
-        return splitzip_kv4_queries(q.data_ptr(), q.stride(0), q.stride(1), q.shape[1], code, min(window or 0, big),
-                                    min(sinks, big), self.head_dim ** -0.5 if scale is None else scale)
+        stride = q.stride()
+        return splitzip_kv4_queries(q.data_ptr(), stride[0], stride[1], q.shape[1], code, min(window or 0, _BIG),
+                                    sinks if sinks < _BIG else _BIG, self.head_dim ** -0.5 if scale is None else scale)
 
-    def _stream(self):
-        import torch
-        return torch._C._cuda_getCurrentRawStream(self.device.index or 0) or None
+    def _contiguous_like(self, t):
+        """An uninitialized contiguous tensor of t's shape and type."""
+        return self._empty_like(t) if t.is_contiguous() else self._empty(t.shape, dtype=t.dtype, device=self.device)
 
     # -- operators --------------------------------------------------------------------------
     def append(self, k, v, table, lens, cu=None):
@@ -204,14 +210,16 @@ class KV4Cache:
         if self._rows(v, "v", self.kv_heads) != code or v.shape != k.shape:
             raise ValueError("k and v must have the same shape and type")
         b = self._batch(table, lens, cu, k.shape[0], None, None)
-        _check(self._L.splitzip_kv4_append(self._ref, ctypes.byref(b), k.data_ptr(), k.stride(0), k.stride(1),
-                                           v.data_ptr(), v.stride(0), v.stride(1), code, self._stream()))
+        sk, sv = k.stride(), v.stride()
+        _check(self._L.splitzip_kv4_append(self._ref, ctypes.byref(b), k.data_ptr(), sk[0], sk[1], v.data_ptr(), sv[0],
+                                           sv[1], code, self._stream(self._index)))
 
     def read(self, table, lens, cu=None, total=None, dtype=None):
         """k and v [total, kv_heads, head_dim] as the cache holds them at the sequences' last tokens.
         ``total``: rows, cu[-1] (without cu: one a sequence).  Rows at no token read as NaN."""
-        import torch
-        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype is None:
+            import torch
+            dtype = torch.bfloat16
         if dtype not in self._dtypes:
             raise TypeError(f"dtype must be bf16, fp16 or fp32, got {dtype}")
         if total is None:
@@ -219,10 +227,10 @@ class KV4Cache:
                 raise ValueError("total (the rows, cu[-1]) must be given with cu")
             total = table.shape[0]
         b = self._batch(table, lens, cu, total, None, None)
-        k = torch.empty(total, self.kv_heads, self.head_dim, dtype=dtype, device=self.device)
-        v = torch.empty_like(k)
+        k = self._empty((total, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
+        v = self._empty_like(k)
         _check(self._L.splitzip_kv4_read(self._ref, ctypes.byref(b), k.data_ptr(), v.data_ptr(), self._dtypes[dtype],
-                                         self._stream()))
+                                         self._stream(self._index)))
         return k, v
 
     def attend(self, q, table, lens, cu=None, max_q=None, max_len=None, scale=None, window=None, sinks=0):
@@ -231,46 +239,45 @@ class KV4Cache:
         tokens j <= p with j > p - window (None: all) or j < sinks.  A query that sees nothing gets
         out = 0, lse = -inf.  ``scale``: default head_dim ** -0.5.  ``max_q`` and ``max_len`` (most
         queries and tokens of a sequence, from the host) only choose the launch."""
-        import torch
         qs = self._queries(q, scale, window, sinks)
-        b = self._batch(table, lens, cu, q.shape[0], max_q, max_len)
-        need = ctypes.c_uint64()
-        _check(self._L.splitzip_kv4_attend_workspace(self._ref, ctypes.byref(b), ctypes.byref(qs), ctypes.byref(need)))
-        out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
-        work = torch.empty(need.value, dtype=torch.uint8, device=self.device) if need.value else None
-        _check(self._L.splitzip_kv4_attend(self._ref, ctypes.byref(b), ctypes.byref(qs), out.data_ptr(), lse.data_ptr(),
-                                           work.data_ptr() if work is not None else None, need.value, self._stream()))
+        rows, heads, _ = q.shape
+        b = self._batch(table, lens, cu, rows, max_q, max_len)
+        b_ref, q_ref, need = ctypes.byref(b), ctypes.byref(qs), ctypes.c_uint64()
+        _check(self._L.splitzip_kv4_attend_workspace(self._ref, b_ref, q_ref, ctypes.byref(need)))
+        out = self._contiguous_like(q)
+        lse = self._empty((rows, heads), dtype=self._f32, device=self.device)
+        size = need.value
+        work = self._empty(size // 4, dtype=self._f32, device=self.device) if size else None
+        _check(self._L.splitzip_kv4_attend(self._ref, b_ref, q_ref, out.data_ptr(), lse.data_ptr(),
+                                           work.data_ptr() if size else None, size, self._stream(self._index)))
         return out, lse
 
     def weigh(self, q, lse, table, lens, cu=None, max_q=None, max_len=None, scale=None, window=None, sinks=0):
         """Adds to ``weights`` the attention that every token and KV head got from q: exp(scale q.k - lse)
         over the queries that see it and the heads of its group.  ``lse`` is what ``attend`` gave
         for these queries and masks."""
-        import torch
         qs = self._queries(q, scale, window, sinks)
-        if lse.dtype != torch.float32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous() or \
+        if lse.dtype is not self._f32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous() or \
                 lse.device != self.device:
             raise ValueError(f"lse must be a contiguous float32 {tuple(q.shape[:2])} tensor on {self.device}")
         b = self._batch(table, lens, cu, q.shape[0], max_q, max_len)
-        _check(self._L.splitzip_kv4_weigh(self._ref, ctypes.byref(b), ctypes.byref(qs), lse.data_ptr(), self._stream()))
+        _check(self._L.splitzip_kv4_weigh(self._ref, ctypes.byref(b), ctypes.byref(qs), lse.data_ptr(), self._stream(self._index)))
 
     def evict(self, table, lens, out_table, budget: int, sinks: int = 0, recent: int = 0, max_len=None):
         """Cuts every sequence to ``budget`` tokens a KV head: its first ``sinks``, its last ``recent`` and
         the tokens of the largest weights between (the lowest first among equals).  They move, in
         token order, to the pages of ``out_table`` (none of which may be in ``table``)
         -> (out_lens int32 [seqs], kept int32 [seqs, kv_heads, budget], -1 behind the last)."""
-        import torch
         if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
             raise ValueError("budget must be at least 1 and hold sinks and recent")
         b = self._batch(table, lens, None, table.shape[0], None, max_len)
         if out_table.dim() != 2 or out_table.shape[0] != table.shape[0]:
             raise ValueError("out_table must be [seqs, pages]")
-        out_lens = torch.empty(table.shape[0], dtype=torch.int32, device=self.device)
-        kept = torch.empty(table.shape[0], self.kv_heads, budget, dtype=torch.int32, device=self.device)
+        out_lens = self._empty(table.shape[0], dtype=self._i32, device=self.device)
+        kept = self._empty((table.shape[0], self.kv_heads, budget), dtype=self._i32, device=self.device)
         _check(self._L.splitzip_kv4_evict(self._ref, ctypes.byref(b), self._int32(out_table, "out_table"),
                                           out_table.stride(0), out_table.shape[1], budget, sinks, recent,
-                                          out_lens.data_ptr(), kept.data_ptr(), self._stream()))
+                                          out_lens.data_ptr(), kept.data_ptr(), self._stream(self._index)))
         return out_lens, kept
 
     def check(self) -> None:
