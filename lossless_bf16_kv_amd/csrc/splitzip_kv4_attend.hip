@@ -13,8 +13,8 @@
 //
 // Two kernels.  few_rows: up to 16 rows a sequence and KV head (a decode step).  HBM bounds it:
 // 1.06 bytes a channel pair of K and V against 64 flops.  Each wave takes pairs of groups of its
-// own, holds the codes of the next pair in registers while it works on this one, and uses no LDS
-// until the four waves' results are joined.  many_rows: 64 or 128 rows a workgroup (drafts,
+// own, has the codes of the next two on their way to LDS while it works on this one, and waits for no
+// other wave until their results are joined.  many_rows: 64 or 128 rows a workgroup (drafts,
 // prefill chunks).  Each wave converts one group of every 64 tokens into matrix operands in LDS,
 // which all four waves use: conversion would else cost as much as the products.
 //
@@ -32,18 +32,21 @@ namespace {
 
 constexpr int kLanes = 256;
 
-// Workgroup b -> sequence, row tile, KV head and split.
+// Workgroup b -> KV head, row tile, sequence and split, the head fastest: workgroups go to the eight
+// XCDs in turn, so each gets the same share of long and short sequences (with the split fastest one
+// XCD in four got the late splits that few sequences have: 310 us for 265), and tiles that read the
+// same keys and values meet in one L2.
 struct Place {
     int s, head, tile, split;
     __device__ Place(const AttendArgs &a)
     {
         uint32_t b = blockIdx.x;
-        split = b % a.splits;
-        b /= a.splits;
+        head = b % a.c.heads;
+        b /= a.c.heads;
         tile = b % a.tiles;
         b /= a.tiles;
-        head = b % a.c.heads;
-        s = b / a.c.heads;
+        s = b % a.b.n_seqs;
+        split = b / a.b.n_seqs;
     }
 };
 
@@ -73,13 +76,23 @@ __device__ void fill_unowned(const AttendArgs &a, const Place &at)
     }
 }
 
-// The part of `count` groups that a split takes: [first, last).
-__device__ __forceinline__ void share(int count, int splits, int split, int unit, int &first, int &last)
+// The part of `count` groups that a split takes: [first, last).  `used` splits have one; what the
+// launch did not expect goes to the last.  A split that has all of them writes the result itself.
+struct Share {
+    int first, last, used;
+    __device__ Share(const AttendArgs &a, int count, int split)
+    {
+        used = max(1, min(a.splits, (count + a.per - 1) / a.per));
+        first = min(count, split * a.per);
+        last = split == used - 1 ? count : min(count, first + a.per);
+    }
+};
+
+// The groups that rows row0 .. of a sequence's tile see.
+__device__ __forceinline__ Groups tile_groups(const AttendArgs &a, const Seq &q, int row0, int tile_rows)
 {
-    const int units = (count + unit - 1) / unit;
-    const int per = (units + splits - 1) / splits;
-    first = min(count, split * per * unit);
-    last = min(count, first + per * unit);
+    const int rows = q.n * a.group, base = q.len - q.n;
+    return Groups(base + row0 / a.group, base + min(row0 + tile_rows - 1, rows - 1) / a.group, a.window, a.sinks);
 }
 
 // Scores are scaled by a positive number: a negative scale's sign goes to the queries, and a scale of
@@ -143,15 +156,167 @@ struct Pair {
     int ga, gb;          // groups; -1: none, or on a bad page
 };
 
+// A pair's codes and scales in LDS, written there by loads that need no registers, so that two pairs
+// of every wave are on their way at a time:
+//   K of both groups, V of both groups, D / 32 * 256 bytes each
+//     D >= 128: 16 bytes a lane in lane order (D = 256: two of them); D = 64: as in the cache
+//   scales: K's of both groups (as in the cache), V's of both groups [block][token], D / 2 bytes each
+template <int D>
+struct Ring {
+    static constexpr int kCodes = 8 * D, kScales = D / 2, kBytes = 4 * kCodes + 4 * kScales;
+    static constexpr int kLoads = D == 64 ? 3 : D == 128 ? 5 : 10;       // instructions a pair
+    uint8_t slot[2][kBytes];
+};
+
+typedef __attribute__((address_space(1))) const void *global_ptr;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+
+// 16 or 4 bytes a lane, in lane order.
+__device__ __forceinline__ void to_lds16(const uint8_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ void to_lds4(const uint8_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 4, 0, 0);
+}
+
+// Groups ga and gb (on pages pa and pb; -1: page 0's tokens) to a slot.
+template <int D>
+__device__ __forceinline__ void send_pair(const Cache &c, int pa, int pb, int head, int ga, int gb, uint32_t lane, uint8_t *slot)
+{
+    constexpr int kCodes = Ring<D>::kCodes;
+    const uint32_t r = lane & 15, quad = lane >> 4;
+    const int64_t ta = group_first(c, pa, head, ga), tb = group_first(c, pb, head, gb);
+    const int64_t a0 = ta >> c.page_shift << c.page_shift, b0 = tb >> c.page_shift << c.page_shift;
+    const uint8_t *const va = c.v_scales + a0 * (D / 32) + (ta - a0), *const vb = c.v_scales + b0 * (D / 32) + (tb - b0);
+    if constexpr (D == 64) {
+        // one load for both groups: lanes 32 .. 63 take the second
+        const int64_t t = lane < 32 ? ta : tb;
+        to_lds16(c.k_codes + t * 32 + 16 * (lane & 31), slot);
+        to_lds16(c.v_codes + t * 32 + 16 * (lane & 31), slot + 2 * kCodes);
+        if (lane < 32) {
+            const uint32_t x = lane & 7;
+            const uint8_t *const ks = c.k_scales + (lane & 8 ? tb : ta) * 2 + 4 * x;
+            const uint8_t *const vs = (lane & 8 ? vb : va) + (x >> 2 << c.page_shift) + 4 * (x & 3);
+            to_lds4(lane < 16 ? ks : vs, slot + 4 * kCodes);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 128; ++i) {
+            const uint32_t k = r * (D / 2) + quad * (D / 8) + 16 * i, v = quad * (2 * D) + r * (D / 8) + 16 * i;
+            to_lds16(lane_at(c.k_codes + ta * (D / 2), k), slot + 1024 * i);
+            to_lds16(lane_at(c.k_codes + tb * (D / 2), k), slot + kCodes + 1024 * i);
+            to_lds16(lane_at(c.v_codes + ta * (D / 2), v), slot + 2 * kCodes + 1024 * i);
+            to_lds16(lane_at(c.v_codes + tb * (D / 2), v), slot + 3 * kCodes + 1024 * i);
+        }
+        if constexpr (D == 128) {
+            const uint8_t *const ks = c.k_scales + (lane & 16 ? tb : ta) * 4 + 4 * r;
+            const uint8_t *const vs = (lane & 16 ? vb : va) + (r >> 2 << c.page_shift) + 4 * (r & 3);
+            to_lds4(lane < 32 ? ks : vs, slot + 4 * kCodes);
+        } else {
+            const uint32_t x = lane & 31;
+            to_lds4(c.k_scales + (lane < 32 ? ta : tb) * 8 + 4 * x, slot + 4 * kCodes);
+            to_lds4((lane < 32 ? va : vb) + (x >> 2 << c.page_shift) + 4 * (x & 3), slot + 4 * kCodes + 256);
+        }
+    }
+}
+
+// A slot's pair to registers, once its loads are done: all but the Younger instructions behind them.
+// The compiler would wait for every load to LDS before it reads there, so waits and reads are one
+// piece of assembly.
+template <int D, int Younger>
+__device__ __forceinline__ void take_pair(const uint8_t *slot, uint32_t lane, Pair<D> &p)
+{
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t r = lane & 15, quad = lane >> 4;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)slot;
+    if constexpr (D == 64) {
+        const uint32_t k = base + r * 32 + quad * 8, v = base + quad * 128 + r * 8;
+        const uint32_t ks = base + r * 2 + (quad >> 1), vs = base + (r >> 3) * 16 + quad * 4;
+        u32x2 a, b, c, d;
+        asm volatile("s_waitcnt vmcnt(%12)\n"
+                     "ds_read_b64 %0, %8\n"
+                     "ds_read_b64 %1, %8 offset:512\n"
+                     "ds_read_b64 %2, %9 offset:1024\n"
+                     "ds_read_b64 %3, %9 offset:1536\n"
+                     "ds_read_u8 %4, %10 offset:2048\n"
+                     "ds_read_u8 %5, %10 offset:2080\n"
+                     "ds_read_b32 %6, %11 offset:2112\n"
+                     "ds_read_b32 %7, %11 offset:2144\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(p.ka.s), "=&v"(p.kb.s), "=&v"(p.va.s), "=&v"(p.vb.s)
+                     : "v"(k), "v"(v), "v"(ks), "v"(vs), "n"(Younger)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            p.ka.w[i] = a[i]; p.kb.w[i] = b[i]; p.va.w[i] = c[i]; p.vb.w[i] = d[i];
+        }
+    } else if constexpr (D == 128) {
+        const uint32_t k = base + 16 * lane, ks = base + r * 4 + quad, vs = base + (r >> 2) * 16 + quad * 4;
+        u32x4 a, b, c, d;
+        asm volatile("s_waitcnt vmcnt(%11)\n"
+                     "ds_read_b128 %0, %8\n"
+                     "ds_read_b128 %1, %8 offset:1024\n"
+                     "ds_read_b128 %2, %8 offset:2048\n"
+                     "ds_read_b128 %3, %8 offset:3072\n"
+                     "ds_read_u8 %4, %9 offset:4096\n"
+                     "ds_read_u8 %5, %9 offset:4160\n"
+                     "ds_read_b32 %6, %10 offset:4224\n"
+                     "ds_read_b32 %7, %10 offset:4288\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(p.ka.s), "=&v"(p.kb.s), "=&v"(p.va.s), "=&v"(p.vb.s)
+                     : "v"(k), "v"(ks), "v"(vs), "n"(Younger)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p.ka.w[i] = a[i]; p.kb.w[i] = b[i]; p.va.w[i] = c[i]; p.vb.w[i] = d[i];
+        }
+    } else {
+        const uint32_t k = base + 16 * lane, ks = base + r * 8 + 2 * quad, vs = base + (r >> 1) * 16 + quad * 4;
+        u32x4 a, b, c, d, e, f, g, h;
+        asm volatile("s_waitcnt vmcnt(%15)\n"
+                     "ds_read_b128 %0, %12\n"
+                     "ds_read_b128 %1, %12 offset:1024\n"
+                     "ds_read_b128 %2, %12 offset:2048\n"
+                     "ds_read_b128 %3, %12 offset:3072\n"
+                     "ds_read_b128 %4, %12 offset:4096\n"
+                     "ds_read_b128 %5, %12 offset:5120\n"
+                     "ds_read_b128 %6, %12 offset:6144\n"
+                     "ds_read_b128 %7, %12 offset:7168\n"
+                     "ds_read_u16 %8, %13 offset:8192\n"
+                     "ds_read_u16 %9, %13 offset:8320\n"
+                     "ds_read_b32 %10, %14 offset:8448\n"
+                     "ds_read_b32 %11, %14 offset:8576\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(p.ka.s),
+                       "=&v"(p.kb.s), "=&v"(p.va.s), "=&v"(p.vb.s)
+                     : "v"(k), "v"(ks), "v"(vs), "n"(Younger)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p.ka.w[i] = a[i]; p.ka.w[4 + i] = b[i]; p.kb.w[i] = c[i]; p.kb.w[4 + i] = d[i];
+            p.va.w[i] = e[i]; p.va.w[4 + i] = f[i]; p.vb.w[i] = g[i]; p.vb.w[4 + i] = h[i];
+        }
+    }
+}
+
 // 16 * Cols rows a workgroup.
 template <int D, int T, int Cols>
-__global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs a)
+__global__ __launch_bounds__(kLanes, D == 256 ? 1 : Cols == 2 ? 2 : T == SPLITZIP_KV4_BF16 ? 4 : 3) void few_rows(AttendArgs a)
 {
     constexpr int kHalves = T == SPLITZIP_KV4_FP16 ? 2 : 1;
     constexpr int kSteps = D / 32, kTiles = D / 16;
     constexpr int kRows = 16 * Cols;
     constexpr int kPitch = D + 4;
-    __shared__ float sh_o[4][16][kPitch];
+    // a wave's ring and, behind it in time, its results
+    __shared__ __align__(16) union Buffer {
+        Ring<D> ring;
+        float o[16][kPitch];
+        __device__ Buffer() {}
+    } sh[4];
     __shared__ float sh_m[4][16], sh_l[4][16];
 
     const Place at(a);
@@ -181,9 +346,11 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
                     qf[c][1][st] = scale(q_frag<T, 1>(a.q, p + 8 * st, a.wide));
             }
         }
-        const Groups groups(q_lo, q_hi, a.window, a.sinks);
-        int first, last;
-        share(groups.count, a.splits, at.split, 8, first, last);
+        const Groups groups = tile_groups(a, q, row0, kRows);
+        const Share share(a, groups.count, at.split);
+        if (at.split >= share.used)
+            continue;
+        const int first = share.first, last = share.last;
 
         float m[Cols], l[Cols];
         uint32_t lost[Cols];                     // blocks whose result is a NaN
@@ -200,28 +367,30 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
 
         Pages pages_a, pages_b;
         const int v0 = first + 2 * wave;
-        auto fetch = [&](int i) {
-            Pair<D> p;
-            const int v = v0 + 8 * i;
+        auto group = [&](int v) { return v < last ? groups.at(v) : -1; };
+        const int turns = v0 < last ? (last - v0 + 7) >> 3 : 0;
+        uint32_t missing = 0;                    // bits 2 i, 2 i + 1: the groups of slot i have no page
+        auto send = [&](int i) {
+            const int v = v0 + 8 * i, slot = i & 1;
             const int pa = pages_a.at(a.c, a.b, at.s, groups, v0, 8, last, i);
             const int pb = pages_b.at(a.c, a.b, at.s, groups, v0 + 1, 8, last, i);
-            p.ga = v < last ? groups.at(v) : -1;
-            p.gb = v + 1 < last ? groups.at(v + 1) : -1;
-            p.ka = load_k<D>(a.c, pa, at.head, p.ga, lane);
-            p.kb = load_k<D>(a.c, pb, at.head, p.gb, lane);
-            p.va = load_v<D>(a.c, pa, at.head, p.ga, lane, quad);
-            p.vb = load_v<D>(a.c, pb, at.head, p.gb, lane, quad);
-            p.ga = pa < 0 ? -1 : p.ga;
-            p.gb = pb < 0 ? -1 : p.gb;
-            return p;
+            missing = (missing & ~(3u << (2 * slot))) | ((pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u)) << (2 * slot);
+            send_pair<D>(a.c, pa, pb, at.head, group(v), group(v + 1), lane, sh[wave].ring.slot[slot]);
         };
-        Pair<D> next;
-        if (v0 < last)
-            next = fetch(0);
-        for (int n = 0; v0 + 8 * n < last; ++n) {
-            Pair<D> cur = next;
-            if (v0 + 8 * n + 8 < last)
-                next = fetch(n + 1);
+        if (turns > 0)
+            send(0);
+        if (turns > 1)
+            send(1);
+        for (int n = 0; n < turns; ++n) {
+            Pair<D> cur;
+            if (n + 1 < turns)
+                take_pair<D, Ring<D>::kLoads>(sh[wave].ring.slot[n & 1], lane, cur);
+            else
+                take_pair<D, 0>(sh[wave].ring.slot[n & 1], lane, cur);
+            cur.ga = missing >> (2 * (n & 1)) & 1 ? -1 : group(v0 + 8 * n);
+            cur.gb = missing >> (2 * (n & 1)) & 2 ? -1 : group(v0 + 8 * n + 1);
+            if (n + 2 < turns)
+                send(n + 2);
             f32x4 sa[Cols], sb[Cols];
 #pragma unroll
             for (int c = 0; c < Cols; ++c)
@@ -322,7 +491,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
 #pragma unroll
                 for (int t = 0; t < kTiles; t += 4) {
                     const f32x4 x = {o[c][t][i], o[c][t + 1][i], o[c][t + 2][i], o[c][t + 3][i]};
-                    *(f32x4 *)&sh_o[wave][r][(4 * quad + i) * kTiles + t] = x;
+                    *(f32x4 *)&sh[wave].o[r][(4 * quad + i) * kTiles + t] = x;
                 }
             __syncthreads();
             const int orow = threadIdx.x >> 4, part = threadIdx.x & 15;
@@ -344,11 +513,11 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
 #pragma unroll
                 for (int k = 0; k < D; k += 64) {
                     const int d = k + 4 * part;
-                    f32x4 x = *(const f32x4 *)&sh_o[0][orow][d] * f[0];
+                    f32x4 x = *(const f32x4 *)&sh[0].o[orow][d] * f[0];
 #pragma unroll
                     for (int w = 1; w < 4; ++w)
-                        x += *(const f32x4 *)&sh_o[w][orow][d] * f[w];
-                    if (a.splits == 1) {
+                        x += *(const f32x4 *)&sh[w].o[orow][d] * f[w];
+                    if (share.used == 1) {
                         x *= inv;
                         *(uint2 *)((uint16_t *)a.out + g * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
                     } else {
@@ -356,7 +525,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : 2) void few_rows(AttendArgs 
                     }
                 }
                 if (part == 0) {
-                    if (a.splits == 1) {
+                    if (share.used == 1) {
                         if (a.lse)
                             a.lse[g] = sum == 0.0f ? -INFINITY : (big + __log2f(sum)) * kLn2;
                     } else {
@@ -421,9 +590,11 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
     for (int n = at.tile; n < row_tiles; n += a.tiles) {
         const int row0 = (row_tiles - 1 - n) * kRows;
         const int base = q.len - q.n;
-        const Groups groups(base + row0 / a.group, base + min(row0 + kRows - 1, rows - 1) / a.group, a.window, a.sinks);
-        int first, last;
-        share(groups.count, a.splits, at.split, kWaves, first, last);
+        const Groups groups = tile_groups(a, q, row0, kRows);
+        const Share share(a, groups.count, at.split);
+        if (at.split >= share.used)
+            continue;
+        const int first = share.first, last = share.last;
 
         // this wave's rows; a row past the end repeats the last and is not stored
         const int w_row = row0 + wave % Rows * 32;
@@ -673,7 +844,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
 #pragma unroll
                 for (int c = 0; c < D / 16; c += 4) {
                     f32x4 y = {o[c / 2][i], o[c / 2][8 + i], o[c / 2 + 1][i], o[c / 2 + 1][8 + i]};
-                    if (a.splits == 1) {
+                    if (share.used == 1) {
                         y *= inv;
                         *(uint2 *)((uint16_t *)a.out + gr * D + d + c) = make_uint2(to_type(y[0], y[1], T), to_type(y[2], y[3], T));
                     } else {
@@ -682,7 +853,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                 }
             }
             if (half == 0) {
-                if (a.splits == 1) {
+                if (share.used == 1) {
                     if (a.lse)
                         a.lse[gr] = l == 0.0f ? -INFINITY : (m + __log2f(l)) * kLn2;
                 } else {
@@ -706,42 +877,51 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
     const int64_t rows = a.b.total * a.q_heads;
     const int64_t row = (int64_t)blockIdx.x * (kLanes / kRow) + threadIdx.x / kRow;
     const int part = threadIdx.x % kRow, d = 4 * part;
-    // rows of no sequence: fill_unowned wrote them.  All lanes stay for the shuffles.
-    const bool mine = row < rows && sequence_of(a.b, row / a.q_heads) >= 0;
-    const int64_t from = row < rows ? row : 0;
+    // Rows of no sequence fill_unowned wrote, those of one split that split did.  All lanes stay for the
+    // shuffles.
+    int splits = 0;
+    const int64_t i = row / a.q_heads;
+    const int seq = row < rows ? sequence_of(a.b, i) : -1;
+    if (seq >= 0) {
+        const Seq q = sequence(a.c, a.b, seq);
+        const int r = (int)(i - q.row0) * a.group + (int)(row % a.q_heads) % a.group;
+        splits = Share(a, tile_groups(a, q, r / a.tile_rows * a.tile_rows, a.tile_rows).count, 0).used;
+    }
+    const bool mine = splits > 1;
+    const int64_t from = mine ? row : 0;
     // O of eight splits at a time, the first on their way before the factors are known
     f32x4 y[8];
     auto load = [&](int s) {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            y[e] = *(const f32x4 *)(a.part_o + (min(s + e, a.splits - 1) * rows + from) * D + d);
+            y[e] = s + e < splits ? *(const f32x4 *)(a.part_o + ((s + e) * rows + from) * D + d) : f32x4{0, 0, 0, 0};
     };
     load(0);
     float big = -INFINITY;
-    for (int s = part; s < a.splits; s += kRow)
+    for (int s = part; s < splits; s += kRow)
         big = fmaxf(big, a.part_ml[(s * rows + from) * 2]);
 #pragma unroll
     for (int x = 1; x < kRow; x *= 2)
         big = fmaxf(big, __shfl_xor(big, x));
     float sum = 0.0f;
     f32x4 x = {0, 0, 0, 0};
-    for (int s0 = 0; s0 < a.splits; s0 += kRow) {
+    for (int s0 = 0; __any(s0 < splits); s0 += kRow) {
         const int s = s0 + part;
         float f = 0.0f, l = 0.0f;
-        if (s < a.splits) {
+        if (s < splits) {
             const float m = a.part_ml[(s * rows + from) * 2];
             // m = -infinity: the split saw nothing, or NaN scores alone, which its sum holds
             f = big == -INFINITY ? 1.0f : exp2_fast(m - big);
             l = a.part_ml[(s * rows + from) * 2 + 1] * f;
         }
-        for (int i = 0; i < kRow && s0 + i < a.splits; i += 8) {
+        for (int i = 0; i < kRow && __any(s0 + i < splits); i += 8) {
             if (s0 + i > 0)
                 load(s0 + i);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float fe = __shfl(f, i + e, kRow);
                 sum += __shfl(l, i + e, kRow);
-                if (s0 + i + e < a.splits)
+                if (s0 + i + e < splits)
                     x += y[e] * fe;
             }
         }
@@ -755,18 +935,18 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
 }
 
 template <int D, int T>
-void attend_dt(const AttendArgs &a, int tile_rows, hipStream_t s)
+void attend_dt(const AttendArgs &a, hipStream_t s)
 {
     const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.tiles * a.splits);
     constexpr int kWaves = D == 256 ? 4 : 8, kLanesMany = 64 * kWaves;
-    if (tile_rows == 16)
+    if (a.tile_rows == 16)
         few_rows<D, T, 1><<<grid, kLanes, 0, s>>>(a);
-    else if (tile_rows == 32) {
+    else if (a.tile_rows == 32) {
         if constexpr (D < 256)
             few_rows<D, T, 2><<<grid, kLanes, 0, s>>>(a);
-    } else if (tile_rows == 64)
+    } else if (a.tile_rows == 64)
         many_rows<D, T, kWaves, 2><<<grid, kLanesMany, 0, s>>>(a);
-    else if (tile_rows == 128)
+    else if (a.tile_rows == 128)
         many_rows<D, T, kWaves, 4><<<grid, kLanesMany, 0, s>>>(a);
     else if constexpr (D < 256)
         many_rows<D, T, kWaves, 8><<<grid, kLanesMany, 0, s>>>(a);
@@ -777,12 +957,12 @@ void attend_dt(const AttendArgs &a, int tile_rows, hipStream_t s)
 }
 
 template <int D>
-void attend_d(const AttendArgs &a, int dtype, int tile_rows, hipStream_t s)
+void attend_d(const AttendArgs &a, int dtype, hipStream_t s)
 {
     if (dtype == SPLITZIP_KV4_BF16)
-        attend_dt<D, SPLITZIP_KV4_BF16>(a, tile_rows, s);
+        attend_dt<D, SPLITZIP_KV4_BF16>(a, s);
     else
-        attend_dt<D, SPLITZIP_KV4_FP16>(a, tile_rows, s);
+        attend_dt<D, SPLITZIP_KV4_FP16>(a, s);
 }
 
 }  // namespace
@@ -792,11 +972,11 @@ int attend_rows(int head_dim, int64_t rows)
     return rows <= 16 ? 16 : rows <= 32 && head_dim < 256 ? 32 : rows <= 64 ? 64 : rows <= 128 || head_dim == 256 ? 128 : 256;
 }
 
-void launch_attend(const AttendArgs &a, int head_dim, int dtype, int tile_rows, hipStream_t s)
+void launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s)
 {
-    head_dim == 64    ? attend_d<64>(a, dtype, tile_rows, s)
-    : head_dim == 128 ? attend_d<128>(a, dtype, tile_rows, s)
-                      : attend_d<256>(a, dtype, tile_rows, s);
+    head_dim == 64    ? attend_d<64>(a, dtype, s)
+    : head_dim == 128 ? attend_d<128>(a, dtype, s)
+                      : attend_d<256>(a, dtype, s);
 }
 
 }  // namespace kv4

@@ -107,23 +107,28 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
     return SPLITZIP_OK;
 }
 
-// Launch of an attend call: rows of a workgroup, row tiles, splits along the tokens.
-int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzip_kv4_queries *q, AttendArgs *a,
-         int *tile_rows)
+// Launch of an attend call: rows of a workgroup, row tiles, splits along the tokens.  The lengths are
+// known only to the GPU.  A split takes 4096 tokens, so that a few long sequences among short ones do
+// not outlast the others (256 decode steps of 128 .. 8192 tokens: 251 us, unsplit 263, at 2048 264);
+// fewer, but 256 at least, where there would be fewer workgroups than the GPU holds at a time.
+int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzip_kv4_queries *q, AttendArgs *a)
 {
     const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
-    *tile_rows = attend_rows(c->head_dim, rows);
+    a->tile_rows = attend_rows(c->head_dim, rows);
     const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
-    int64_t tiles = ceil_div(rows, *tile_rows);
+    int64_t tiles = ceil_div(rows, a->tile_rows);
     KV4_REQUIRE(pairs <= INT32_MAX / 4, "too many sequences and heads");
     tiles = std::min<int64_t>(tiles, std::max<int64_t>(1, INT32_MAX / 4 / std::max<int64_t>(1, pairs)));
     int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
     if (q->window > 0)
         tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
-    const int64_t blocks = std::max<int64_t>(1, pairs * tiles);
-    const int64_t splits = std::min<int64_t>(ceil_div(tokens, 256), (*tile_rows <= 32 ? 1024 : 512) / blocks);
+    const int64_t blocks = std::max<int64_t>(1, pairs * tiles), fill = a->tile_rows <= 32 ? 1024 : 512;
+    int64_t splits = std::max(std::min(ceil_div(tokens, 256), fill / blocks), a->tile_rows <= 32 ? ceil_div(tokens, 4096) : 1);
+    splits = std::min(std::max<int64_t>(1, splits), INT32_MAX / 4 / blocks);
+    const int64_t groups = ceil_div(std::max<int64_t>(1, tokens), 16);
+    a->per = (int32_t)(ceil_div(ceil_div(groups, splits), 8) * 8);
     a->tiles = (int32_t)tiles;
-    a->splits = (int32_t)std::max<int64_t>(1, splits);
+    a->splits = (int32_t)ceil_div(groups, a->per);
     return SPLITZIP_OK;
 }
 
@@ -195,7 +200,6 @@ int splitzip_kv4_attend_workspace(const splitzip_kv4_cache *cache, const splitzi
                                   const splitzip_kv4_queries *queries, uint64_t *bytes)
 {
     AttendArgs a;
-    int rows;
     KV4_REQUIRE(bytes, "bytes is null");
     if (int e = check_cache(cache, &a.c))
         return e;
@@ -203,7 +207,7 @@ int splitzip_kv4_attend_workspace(const splitzip_kv4_cache *cache, const splitzi
         return e;
     if (int e = check_queries(queries, batch, cache, &a))
         return e;
-    if (int e = plan(cache, batch, queries, &a, &rows))
+    if (int e = plan(cache, batch, queries, &a))
         return e;
     *bytes = workspace_of(a, cache->head_dim);
     return SPLITZIP_OK;
@@ -214,7 +218,6 @@ int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
                         uint64_t workspace_bytes, void *stream)
 {
     AttendArgs a;
-    int rows;
     if (int e = check_cache(cache, &a.c))
         return e;
     if (int e = check_batch(batch, a.c, true, &a.b))
@@ -224,7 +227,7 @@ int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
     if (a.b.total == 0)
         return SPLITZIP_OK;
     KV4_REQUIRE(out && aligned16(out), "out is null or not 16-byte aligned");
-    if (int e = plan(cache, batch, queries, &a, &rows))
+    if (int e = plan(cache, batch, queries, &a))
         return e;
     const uint64_t need = workspace_of(a, cache->head_dim);
     KV4_REQUIRE(need == 0 || (workspace && aligned16(workspace) && workspace_bytes >= need),
@@ -236,7 +239,7 @@ int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
     Device d(cache->device);
     if (d.status)
         return d.status;
-    launch_attend(a, cache->head_dim, queries->dtype, rows, static_cast<hipStream_t>(stream));
+    launch_attend(a, cache->head_dim, queries->dtype, static_cast<hipStream_t>(stream));
     return Device::launched();
 }
 

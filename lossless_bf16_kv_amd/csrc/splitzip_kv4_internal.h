@@ -54,6 +54,7 @@ struct AttendArgs {
     const float *lse_in;     // weigh
     float *part_o, *part_ml; // partial results of splits > 1: [split][row][D], [split][row][2]
     int32_t splits, tiles;   // workgroups along the tokens and along the rows of a sequence and head
+    int32_t per, tile_rows;  // attend: groups of 16 tokens a split, rows a tile
 };
 
 struct EvictArgs {
@@ -69,7 +70,7 @@ struct EvictArgs {
 void launch_append(const AppendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_read(const ReadArgs &a, int head_dim, int dtype, hipStream_t s);
 int attend_rows(int head_dim, int64_t rows);   // rows of a workgroup for this many rows a sequence
-void launch_attend(const AttendArgs &a, int head_dim, int dtype, int tile_rows, hipStream_t s);
+void launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_weigh(const AttendArgs &a, int head_dim, int dtype, int max_q, int max_len, hipStream_t s);
 void launch_evict(const EvictArgs &a, int head_dim, hipStream_t s);
 

@@ -200,7 +200,7 @@ class KV4Cache:
 
     def _contiguous_like(self, t):
         """An uninitialized contiguous tensor of t's shape and type."""
-        return self._empty_like(t) if t.is_contiguous() else self._empty(t.shape, dtype=t.dtype, device=self.device)
+        return self._empty_like(t) if t.is_contiguous() else self._empty(*t.shape, dtype=t.dtype, device=self.device)
 
     # -- operators --------------------------------------------------------------------------
     def append(self, k, v, table, lens, cu=None):
@@ -227,7 +227,7 @@ class KV4Cache:
                 raise ValueError("total (the rows, cu[-1]) must be given with cu")
             total = table.shape[0]
         b = self._batch(table, lens, cu, total, None, None)
-        k = self._empty((total, self.kv_heads, self.head_dim), dtype=dtype, device=self.device)
+        k = self._empty(total, self.kv_heads, self.head_dim, dtype=dtype, device=self.device)
         v = self._empty_like(k)
         _check(self._L.splitzip_kv4_read(self._ref, ctypes.byref(b), k.data_ptr(), v.data_ptr(), self._dtypes[dtype],
                                          self._stream(self._index)))
@@ -245,7 +245,7 @@ class KV4Cache:
         b_ref, q_ref, need = ctypes.byref(b), ctypes.byref(qs), ctypes.c_uint64()
         _check(self._L.splitzip_kv4_attend_workspace(self._ref, b_ref, q_ref, ctypes.byref(need)))
         out = self._contiguous_like(q)
-        lse = self._empty((rows, heads), dtype=self._f32, device=self.device)
+        lse = self._empty(rows, heads, dtype=self._f32, device=self.device)
         size = need.value
         work = self._empty(size // 4, dtype=self._f32, device=self.device) if size else None
         _check(self._L.splitzip_kv4_attend(self._ref, b_ref, q_ref, out.data_ptr(), lse.data_ptr(),
@@ -274,7 +274,7 @@ class KV4Cache:
         if out_table.dim() != 2 or out_table.shape[0] != table.shape[0]:
             raise ValueError("out_table must be [seqs, pages]")
         out_lens = self._empty(table.shape[0], dtype=self._i32, device=self.device)
-        kept = self._empty((table.shape[0], self.kv_heads, budget), dtype=self._i32, device=self.device)
+        kept = self._empty(table.shape[0], self.kv_heads, budget, dtype=self._i32, device=self.device)
         _check(self._L.splitzip_kv4_evict(self._ref, ctypes.byref(b), self._int32(out_table, "out_table"),
                                           out_table.stride(0), out_table.shape[1], budget, sinks, recent,
                                           out_lens.data_ptr(), kept.data_ptr(), self._stream(self._index)))
