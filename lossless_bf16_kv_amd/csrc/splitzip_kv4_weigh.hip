@@ -55,9 +55,9 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, quad = lane >> 4;
     uint32_t b = blockIdx.x;
-    const int split = b % a.splits;
-    b /= a.splits;
-    const int head = b % a.c.heads, s = b / a.c.heads;
+    const int head = b % a.c.heads;          // fastest: the XCDs get equal shares, and a head's rows meet in one L2
+    b /= a.c.heads;
+    const int s = b % a.b.n_seqs, split = b / a.b.n_seqs;
     const Seq q = wave_sequence(a.c, a.b, s);
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
@@ -173,9 +173,9 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int m32 = lane & 31, half = lane >> 5;
     uint32_t b = blockIdx.x;
-    const int split = b % a.splits;
-    b /= a.splits;
-    const int head = b % a.c.heads, s = b / a.c.heads;
+    const int head = b % a.c.heads;          // fastest: the XCDs get equal shares, and a head's rows meet in one L2
+    b /= a.c.heads;
+    const int s = b % a.b.n_seqs, split = b / a.b.n_seqs;
     const Seq q = wave_sequence(a.c, a.b, s);
     const int rows = q.n * a.group, base = q.len - q.n;
     const Mask mask = {a.window, a.sinks};
@@ -364,8 +364,8 @@ void weigh_dt(AttendArgs a, int max_q, int max_len, hipStream_t s)
 {
     const int64_t pairs = (int64_t)a.b.n_seqs * a.c.heads;
     if ((int64_t)max_q * a.group <= 16) {
-        // 256 tokens a workgroup at least (one turn of each wave), and 4096 workgroups at most
-        const int64_t most = std::max<int64_t>(1, 4096 / pairs);
+        // 256 tokens a workgroup at least (one turn of each wave), and 2048 workgroups at most
+        const int64_t most = std::max<int64_t>(1, 2048 / pairs);
         a.splits = (int32_t)std::min<int64_t>(most, max_len / 256 + 1);
         step_kernel<D, T><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
     } else {
