@@ -284,6 +284,8 @@ int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
     KV4_REQUIRE(out_table && out_lens && kept, "out_table, out_lens or kept is null");
     KV4_REQUIRE(out_table_width >= 0 && (a.b.n_seqs <= 1 || out_table_stride >= out_table_width),
                 "out_table_stride is below out_table_width");
+    // lengths are read while new ones are written
+    KV4_REQUIRE(out_lens + a.b.n_seqs <= a.b.lens || a.b.lens + a.b.n_seqs <= out_lens, "out_lens must not overlap lens");
     KV4_REQUIRE((int64_t)a.b.n_seqs * a.c.heads * ceil_div(budget, 16) < INT32_MAX, "too many tokens to keep");
     a.out_table = out_table;
     a.out_stride = out_table_stride;
