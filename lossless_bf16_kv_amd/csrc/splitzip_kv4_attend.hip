@@ -168,20 +168,6 @@ struct Ring {
     uint8_t slot[2][kBytes];
 };
 
-typedef __attribute__((address_space(1))) const void *global_ptr;
-typedef __attribute__((address_space(3))) void *lds_ptr;
-
-// 16 or 4 bytes a lane, in lane order.
-__device__ __forceinline__ void to_lds16(const uint8_t *from, uint8_t *to)
-{
-    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
-}
-
-__device__ __forceinline__ void to_lds4(const uint8_t *from, uint8_t *to)
-{
-    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 4, 0, 0);
-}
-
 // Groups ga and gb (on pages pa and pb; -1: page 0's tokens) to a slot.
 template <int D>
 __device__ __forceinline__ void send_pair(const Cache &c, int pa, int pb, int head, int ga, int gb, uint32_t lane, uint8_t *slot)

@@ -200,6 +200,23 @@ __device__ __forceinline__ VRaw<D> load_v(const Cache &c, int page, int head, in
     return v;
 }
 
+// ---- loads to LDS ---------------------------------------------------------------------------
+// They need no registers while they are on their way.  A wave waits for them by count, in assembly
+// that also reads them: the compiler would wait for all of them before any read of LDS.
+typedef __attribute__((address_space(1))) const void *global_ptr;
+typedef __attribute__((address_space(3))) void *lds_ptr;
+
+// 16 or 4 bytes a lane, in lane order.
+__device__ __forceinline__ void to_lds16(const uint8_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ void to_lds4(const uint8_t *from, uint8_t *to)
+{
+    __builtin_amdgcn_global_load_lds((global_ptr)from, (lds_ptr)to, 4, 0, 0);
+}
+
 // K operand of step st: channels quad * D / 4 + 8 st .. + 7 of token r.
 template <int D>
 __device__ __forceinline__ bf16x8 k_frag(const KRaw<D> &k, int st)

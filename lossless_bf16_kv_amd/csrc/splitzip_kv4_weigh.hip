@@ -38,20 +38,136 @@ struct RowAt {
 template <int D>
 constexpr int kWeighTokens = D == 256 ? 128 : 256;      // of a workgroup of rows_kernel
 
-// Groups of one turn of a wave, their K, and the weight of the lane's token 16 group[lane / 16] + lane % 16.
+// One turn of a wave in LDS, 64 tokens: K's codes of four groups (8 D bytes each: D >= 128 16 bytes a
+// lane in lane order, D = 256 two of them; D = 64 as in the cache), their scales (D = 64 as in the
+// cache, else 4 bytes a token, D = 256 two such runs) and the tokens' weights.
 template <int D>
 struct Turn {
-    KRaw<D> k[4];
-    int g[4], page[4];
-    float *at;               // null: no token
-    float w;
+    static constexpr int kCodes = 8 * D, kScales = 4 * kCodes, kWeights = kScales + 2 * D, kBytes = kWeights + 256;
+    static constexpr int kLoads = D == 64 ? 4 : D == 128 ? 6 : 11;       // instructions
 };
+
+// Groups g on pages `page` (-1: page 0's tokens) to a slot; t: the lane's token 16 (lane / 16) +
+// lane % 16 of the turn, in the cache.
+template <int D>
+__device__ __forceinline__ void send_turn(const Cache &c, const int (&page)[4], int head, const int (&g)[4], int64_t t,
+                                          uint32_t lane, uint8_t *slot)
+{
+    typedef Turn<D> L;
+    const uint32_t r = lane & 15, quad = lane >> 4;
+    if constexpr (D == 64) {
+        int64_t first[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            first[e] = group_first(c, page[e], head, g[e]);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)      // lanes 32 .. 63 take the second group
+            to_lds16(c.k_codes + (lane < 32 ? first[2 * i] : first[2 * i + 1]) * 32 + 16 * (lane & 31), slot + 1024 * i);
+        const int64_t own = lane < 8 ? first[0] : lane < 16 ? first[1] : lane < 24 ? first[2] : first[3];
+        if (lane < 32)
+            to_lds4(c.k_scales + own * 2 + 4 * (lane & 7), slot + L::kScales);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int i = 0; i < D / 128; ++i)
+                to_lds16(lane_at(c.k_codes + group_first(c, page[e], head, g[e]) * (D / 2), r * (D / 2) + quad * (D / 8) + 16 * i),
+                         slot + e * L::kCodes + 1024 * i);
+#pragma unroll
+        for (int i = 0; i < D / 128; ++i)
+            to_lds4(c.k_scales + t * (D / 32) + 4 * i, slot + L::kScales + 256 * i);
+    }
+    to_lds4((const uint8_t *)(c.weights + t), slot + L::kWeights);
+}
+
+// A slot's turn to registers, once its loads are done: all but the Younger instructions behind them.
+template <int D, int Younger>
+__device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KRaw<D> (&k)[4], float &w)
+{
+    typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+    typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+    const uint32_t r = lane & 15, quad = lane >> 4;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)slot, own = base + 4 * lane;
+    if constexpr (D == 64) {
+        const uint32_t at = base + r * 32 + quad * 8, ks = base + r * 2 + (quad >> 1);
+        u32x2 a, b, c, d;
+        asm volatile("s_waitcnt vmcnt(%12)\n"
+                     "ds_read_b64 %0, %9\n"
+                     "ds_read_b64 %1, %9 offset:512\n"
+                     "ds_read_b64 %2, %9 offset:1024\n"
+                     "ds_read_b64 %3, %9 offset:1536\n"
+                     "ds_read_u8 %4, %10 offset:2048\n"
+                     "ds_read_u8 %5, %10 offset:2080\n"
+                     "ds_read_u8 %6, %10 offset:2112\n"
+                     "ds_read_u8 %7, %10 offset:2144\n"
+                     "ds_read_b32 %8, %11 offset:2176\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s),
+                       "=&v"(w)
+                     : "v"(at), "v"(ks), "v"(own), "n"(Younger)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            k[0].w[i] = a[i]; k[1].w[i] = b[i]; k[2].w[i] = c[i]; k[3].w[i] = d[i];
+        }
+    } else if constexpr (D == 128) {
+        const uint32_t at = base + 16 * lane, ks = base + r * 4 + quad;
+        u32x4 a, b, c, d;
+        asm volatile("s_waitcnt vmcnt(%12)\n"
+                     "ds_read_b128 %0, %9\n"
+                     "ds_read_b128 %1, %9 offset:1024\n"
+                     "ds_read_b128 %2, %9 offset:2048\n"
+                     "ds_read_b128 %3, %9 offset:3072\n"
+                     "ds_read_u8 %4, %10 offset:4096\n"
+                     "ds_read_u8 %5, %10 offset:4160\n"
+                     "ds_read_u8 %6, %10 offset:4224\n"
+                     "ds_read_u8 %7, %10 offset:4288\n"
+                     "ds_read_b32 %8, %11 offset:4352\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s),
+                       "=&v"(w)
+                     : "v"(at), "v"(ks), "v"(own), "n"(Younger)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            k[0].w[i] = a[i]; k[1].w[i] = b[i]; k[2].w[i] = c[i]; k[3].w[i] = d[i];
+        }
+    } else {
+        const uint32_t at = base + 16 * lane, ks = base + r * 4 + (quad >> 1) * 256 + (quad & 1) * 2;
+        u32x4 a, b, c, d, e, f, g, h;
+        asm volatile("s_waitcnt vmcnt(%16)\n"
+                     "ds_read_b128 %0, %13\n"
+                     "ds_read_b128 %1, %13 offset:1024\n"
+                     "ds_read_b128 %2, %13 offset:2048\n"
+                     "ds_read_b128 %3, %13 offset:3072\n"
+                     "ds_read_b128 %4, %13 offset:4096\n"
+                     "ds_read_b128 %5, %13 offset:5120\n"
+                     "ds_read_b128 %6, %13 offset:6144\n"
+                     "ds_read_b128 %7, %13 offset:7168\n"
+                     "ds_read_u16 %8, %14 offset:8192\n"
+                     "ds_read_u16 %9, %14 offset:8256\n"
+                     "ds_read_u16 %10, %14 offset:8320\n"
+                     "ds_read_u16 %11, %14 offset:8384\n"
+                     "ds_read_b32 %12, %15 offset:8704\n"
+                     "s_waitcnt lgkmcnt(0)"
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(k[0].s),
+                       "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s), "=&v"(w)
+                     : "v"(at), "v"(ks), "v"(own), "n"(Younger)
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            k[0].w[i] = a[i]; k[0].w[4 + i] = b[i]; k[1].w[i] = c[i]; k[1].w[4 + i] = d[i];
+            k[2].w[i] = e[i]; k[2].w[4 + i] = f[i]; k[3].w[i] = g[i]; k[3].w[4 + i] = h[i];
+        }
+    }
+}
 
 template <int D, int T>
 __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
 {
     constexpr int kHalves = T == SPLITZIP_KV4_FP16 ? 2 : 1;
     constexpr int kSteps = D / 32;
+    __shared__ __align__(16) uint8_t sh_turn[4][2][Turn<D>::kBytes];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int r = lane & 15, quad = lane >> 4;
     uint32_t b = blockIdx.x;
@@ -96,47 +212,61 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
         const bool every = __all(lse[0] != INFINITY && lse[1] != INFINITY && lse[2] != INFINITY && lse[3] != INFINITY);
 
         int list = -1, from = -16;       // pages of turns from .. + 15: lane 4 i + e has group e of turn i
-        auto fetch = [&](int i) {
+        auto group = [&](int i, int e) {
+            const int v = first + 16 * i + 4 * wave + e;
+            return v < last ? groups.at(v) : -1;
+        };
+        // returns where the weight of the lane's token is, null: no token
+        auto send = [&](int i) {
             if (i >= from + 16) {
                 from = i;
                 const int64_t v = first + 16 * (int64_t)(i + quad * 4 + r / 4) + 4 * wave + r % 4;
                 list = v < last ? page_of(a.c, a.b, s, 16 * groups.at((int)v)) : -1;
             }
-            Turn<D> t;
-            int mine = -1, mine_g = 0;
+            int page[4], g[4], mine = -1, mine_g = -1;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const int v = first + 16 * i + 4 * wave + e;
-                t.page[e] = __builtin_amdgcn_readlane(list, 4 * (i - from) + e);
-                t.g[e] = v < last ? groups.at(v) : -1;
-                t.k[e] = load_k<D>(a.c, t.page[e], head, t.g[e], lane);
-                mine = quad == e ? t.page[e] : mine;
-                mine_g = quad == e ? t.g[e] : mine_g;
+                page[e] = __builtin_amdgcn_readlane(list, 4 * (i - from) + e);
+                g[e] = group(i, e);
+                mine = quad == e ? page[e] : mine;
+                mine_g = quad == e ? g[e] : mine_g;
             }
-            t.at = mine < 0 || 16 * mine_g + r >= q.len ? nullptr : a.c.weights + group_first(a.c, mine, head, mine_g) + r;
-            t.w = t.at ? *t.at : 0.0f;
-            return t;
+            const int64_t t = group_first(a.c, mine, head, mine_g) + r;
+            send_turn<D>(a.c, page, head, g, t, lane, sh_turn[wave][i & 1]);
+            return mine < 0 || 16 * mine_g + r >= q.len ? nullptr : a.c.weights + t;
         };
-        Turn<D> next;
+        if (row0 > 0)
+            __threadfence();             // the rows before have written the weights
+        float *at0 = nullptr, *at1 = nullptr;
         if (turns > 0)
-            next = fetch(0);
+            at0 = send(0);
+        if (turns > 1)
+            at1 = send(1);
         for (int i = 0; i < turns; ++i) {
-            const Turn<D> t = next;
+            KRaw<D> k[4];
+            float w;
             if (i + 1 < turns)
-                next = fetch(i + 1);
+                take_turn<D, Turn<D>::kLoads>(sh_turn[wave][i & 1], lane, k, w);
+            else
+                take_turn<D, 0>(sh_turn[wave][i & 1], lane, k, w);
+            float *const at = at0;
+            at0 = at1;
+            if (i + 2 < turns)
+                at1 = send(i + 2);
             float mine = 0.0f;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 f32x4 x = {0, 0, 0, 0};
 #pragma unroll
                 for (int st = 0; st < kSteps; ++st) {
-                    const bf16x8 f = k_frag<D>(t.k[e], st);
+                    const bf16x8 f = k_frag<D>(k[e], st);
 #pragma unroll
                     for (int h = 0; h < kHalves; ++h)
                         x = mfma(qf[h][st], f, x);
                 }
                 float sum = 0.0f;
-                if (every && mask.all(t.g[e], q_lo, q_hi)) {
+                const int g = group(i, e);
+                if (every && mask.all(g, q_lo, q_hi)) {
 #pragma unroll
                     for (int n = 0; n < 4; ++n)
                         sum += exp2_fast(fmaf(x[n], a.scale2, -lse[n]));
@@ -144,14 +274,14 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
 #pragma unroll
                     for (int n = 0; n < 4; ++n) {
                         const float p = exp2_fast(fmaf(x[n], a.scale2, -lse[n]));
-                        sum += lse[n] != INFINITY && mask.sees(query[n], 16 * t.g[e] + r) ? p : 0.0f;
+                        sum += lse[n] != INFINITY && mask.sees(query[n], 16 * g + r) ? p : 0.0f;
                     }
                 }
                 sum = quad_sum(sum);
                 mine = quad == e ? sum : mine;
             }
-            if (t.at)
-                *t.at = t.w + mine;
+            if (at)
+                *at = w + mine;
         }
     }
 }
