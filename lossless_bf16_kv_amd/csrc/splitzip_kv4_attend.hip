@@ -688,7 +688,10 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                         g[n] = -1;
                     whole = whole && g[n] >= 0 && mask.all(g[n], q_lo, q_hi);
                 }
-                // scores of 32 tokens a tile
+                // scores of 32 tokens a tile, ahead of the other wave's exponentials: the matrix unit idles less
+                // (457 -> 417 us for 4096 queries of 32 heads on 8192 tokens, with the probabilities made before the
+                // second products start)
+                __builtin_amdgcn_s_setprio(1);
                 f32x16 x[kJoin];
                 uint4 code[kJoin][D / 64];
                 uint32_t ks[kJoin];
@@ -719,6 +722,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                             for (int h = 0; h < kHalves; ++h)
                                 x[n] = mfma32(f, qf[h][4 * p + e], x[n]);
                         }
+                __builtin_amdgcn_s_setprio(0);
                 if (!whole) {
 #pragma unroll
                     for (int n = 0; n < kJoin; ++n)
@@ -749,6 +753,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                         o[t] *= f;
                 }
                 const float ref = m == -INFINITY ? 0.0f : m;
+                bf16x8 pf[kJoin][2][kHalves];
 #pragma unroll
                 for (int n = 0; n < kJoin; ++n)
 #pragma unroll
@@ -760,16 +765,19 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                             sum[e & 1] += p[e];
                         }
                         l += sum[0] + sum[1];
-                        bf16x8 pf[kHalves];
-                        p_frag<kHalves>(p, pf);
+                        p_frag<kHalves>(p, pf[n][h]);
+                    }
+#pragma unroll
+                for (int n = 0; n < kJoin; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int t = 0; t < kOut; ++t) {
                             const bf16x8 y = __builtin_bit_cast(bf16x8, st.v[2 * (tile + n) + h][t][lane]);
 #pragma unroll
                             for (int k = 0; k < kHalves; ++k)
-                                o[t] = mfma32(y, pf[k], o[t]);
+                                o[t] = mfma32(y, pf[n][h][k], o[t]);
                         }
-                    }
                 if (notes & 2) {
 #pragma unroll
                     for (int n = 0; n < 2 * kJoin; ++n)
