@@ -82,7 +82,7 @@ struct Share {
     int first, last, used;
     __device__ Share(const AttendArgs &a, int count, int split)
     {
-        used = max(1, min(a.splits, (count + a.per - 1) / a.per));
+        used = max(1, min(a.splits, (int)((uint32_t)(count + a.per - 1) / (uint32_t)a.per)));
         first = min(count, split * a.per);
         last = split == used - 1 ? count : min(count, first + a.per);
     }
@@ -868,21 +868,23 @@ template <int D, int T>
 __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
 {
     constexpr int kRow = D / 4;
-    const int64_t rows = a.b.total * a.q_heads;
-    const int64_t row = (int64_t)blockIdx.x * (kLanes / kRow) + threadIdx.x / kRow;
+    const int64_t rows = a.b.total * a.q_heads;                 // below 2^31
+    const uint32_t row = blockIdx.x * (kLanes / kRow) + threadIdx.x / kRow;
     const int part = threadIdx.x % kRow, d = 4 * part;
     // Rows of no sequence fill_unowned wrote, those of one split that split did.  All lanes stay for the
     // shuffles.
     int splits = 0;
-    const int64_t i = row / a.q_heads;
-    const int seq = row < rows ? sequence_of(a.b, i) : -1;
-    if (seq >= 0) {
-        const Seq q = sequence(a.c, a.b, seq);
-        const int r = (int)(i - q.row0) * a.group + (int)(row % a.q_heads) % a.group;
-        splits = Share(a, tile_groups(a, q, r / a.tile_rows * a.tile_rows, a.tile_rows).count, 0).used;
+    if (row < rows) {
+        const uint32_t i = row / (uint32_t)a.q_heads, f = row - i * a.q_heads;
+        const int seq = sequence_of(a.b, i);
+        if (seq >= 0) {
+            const Seq q = sequence(a.c, a.b, seq);
+            const int r = (int)(i - q.row0) * a.group + (int)(f % (uint32_t)a.group);
+            splits = Share(a, tile_groups(a, q, r & ~(a.tile_rows - 1), a.tile_rows).count, 0).used;
+        }
     }
     const bool mine = splits > 1;
-    const int64_t from = mine ? row : 0;
+    const int64_t from = mine ? (int64_t)row : 0;
     // O of eight splits at a time, the first on their way before the factors are known
     f32x4 y[8];
     auto load = [&](int s) {
@@ -899,6 +901,7 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
         big = fmaxf(big, __shfl_xor(big, x));
     float sum = 0.0f;
     f32x4 x = {0, 0, 0, 0};
+#pragma unroll 1
     for (int s0 = 0; __any(s0 < splits); s0 += kRow) {
         const int s = s0 + part;
         float f = 0.0f, l = 0.0f;
@@ -908,6 +911,7 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
             f = big == -INFINITY ? 1.0f : exp2_fast(m - big);
             l = a.part_ml[(s * rows + from) * 2 + 1] * f;
         }
+#pragma unroll 1
         for (int i = 0; i < kRow && __any(s0 + i < splits); i += 8) {
             if (s0 + i > 0)
                 load(s0 + i);
@@ -923,7 +927,7 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
     if (!mine)
         return;
     x *= sum == 0.0f ? 0.0f : 1.0f / sum;
-    *(uint2 *)((uint16_t *)a.out + row * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
+    *(uint2 *)((uint16_t *)a.out + (int64_t)row * D + d) = make_uint2(to_type(x[0], x[1], T), to_type(x[2], x[3], T));
     if (d == 0 && a.lse)
         a.lse[row] = sum == 0.0f ? -INFINITY : (big + __log2f(sum)) * kLn2;
 }
