@@ -13,7 +13,9 @@
 // Both kernels are bound by HBM: 4 bytes of BF16 K and V to 1.06 bytes of cache and back.  A
 // lane holds 8 channels (one 16-byte load) of K and of V, four lanes share a block.  A workgroup
 // takes 256 * 8 / D consecutive rows of one head, so that the four tokens interleaved in V's
-// layout are written by one workgroup and meet in one L2.
+// layout are written by one workgroup and meet in one L2.  32768 tokens of 8 heads of 128 channels:
+// append 45 us (171 MB, 3.8 TB/s: K and V are slices of a fused projection here, half of every 8 KiB),
+// read 27 us (170 MB, 6.3 TB/s).  Four rows a lane, all loads first, took append 46 us.
 #include "splitzip_kv4_internal.h"
 
 namespace sz {

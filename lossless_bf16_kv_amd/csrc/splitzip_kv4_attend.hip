@@ -11,17 +11,28 @@
 // Rows are pairs of a query and a head of the group (row = query * group + head): the heads of a
 // group share K and V, so they fill the 16 columns of a matrix instruction together.
 //
-// Two kernels.  few_rows: up to 16 rows a sequence and KV head (a decode step).  HBM bounds it:
-// 1.06 bytes a channel pair of K and V against 64 flops.  Each wave takes pairs of groups of its
-// own, has the codes of the next two on their way to LDS while it works on this one, and waits for no
-// other wave until their results are joined.  many_rows: 64 or 128 rows a workgroup (drafts,
-// prefill chunks).  Each wave converts one group of every 64 tokens into matrix operands in LDS,
-// which all four waves use: conversion would else cost as much as the products.
+// Two kernels.  few_rows: up to 16 or 32 rows a sequence and KV head (a decode step, a few drafts).
+// Each wave takes pairs of groups of its own, has the codes of the next two pairs on their way to LDS
+// while it works on this one, and waits for no other wave until their results are joined.  32 decode
+// steps at 32768 tokens (64 heads on 8 of 128 channels): 1.14 GB in 217 us, 5.3 TB/s, 75 % of what
+// reading alone reaches; the same loads into registers: 229 us.  Past that the instructions bound it:
+// 223 vector and 16 matrix ones for 32 tokens, 96 of them conversions.
+//
+// many_rows: 64, 128 or 256 rows a workgroup (long drafts, prefill chunks), which share the conversion
+// of V.  4096 queries of 32 heads on 8192 tokens: 412 GFLOP in 417 us, 0.99 PFLOP/s, three quarters of
+// a large bf16 matrix product's rate here; matrix unit and vector unit are each busy about half of the
+// time, and the rest is what two waves on a unit leave open.  Before: 16-row products with K in LDS as
+// bf16, 1409 us (LDS reads as long as the products); 32-row products and K's codes in LDS, 680; two
+// tiles at a time, 571; heads fastest, so that a head's tiles share an L2, 457.
+//
+// The scaled matrix instructions would take K's codes as they are, and a bf16 query as two e4m3 parts
+// exactly, but their sums over 128 terms are off by up to 2^-13 of the terms' sizes (measured; fp32
+// sums: 2^-17 allowed here), so K becomes bf16 as well.
 //
 // Long axes with few workgroups are split; partial results (m, l, O in 32 bits) are joined by
 // join_kernel in the order of the splits, so results do not depend on timing.
 //
-// Probabilities enter the second product as bf16 (half a step is 2^-9 of the value, as the
+// Probabilities enter the second product as bf16 (half a step is 2^-8 of the value, as the
 // rounding of a bf16 output; the sum l takes them unrounded).  With fp16 queries, queries and
 // probabilities go in as two bf16 halves each, 16 bits in all.
 #include "splitzip_kv4_tiles.h"
@@ -965,6 +976,10 @@ void attend_d(const AttendArgs &a, int dtype, hipStream_t s)
 
 }  // namespace
 
+// Few rows wait for nobody, and waste no products on rows that are not there: drafts of 12 to 24 rows take
+// 35 us by few_rows and 79 us in a tile of 64, decode steps of 8 rows 41 and 92 us.  More rows pay for a
+// shared conversion: 16384 rows 672 us by 64, 511 by 128, 419 by 256.  At 256 channels 32 rows by few_rows
+// and 256 by many_rows would not leave room for two waves' registers.
 int attend_rows(int head_dim, int64_t rows)
 {
     return rows <= 16 ? 16 : rows <= 32 && head_dim < 256 ? 32 : rows <= 64 ? 64 : rows <= 128 || head_dim == 256 ? 128 : 256;

@@ -13,9 +13,9 @@
 //
 // move_kernel gathers codes, scales and weights, 128 tokens a workgroup: every load of a lane is in
 // flight before its first store, since four dependent loads (length, kept token, page, codes) stand
-// before each (16 tokens a workgroup took twice the time).  Its bytes bound it, V's twice where few tokens are kept: a token's 64 bytes of V lie
-// in the 256 bytes that it shares with three others.  512 heads of 128 .. 8192 tokens cut to 2048
-// move 280 MB in 72 us (3.9 TB/s of those bytes alone).
+// before each (16 tokens a workgroup took twice the time).  Memory bounds it, by lines rather than
+// bytes: a token's 64 bytes of V lie in the 256 that it shares with three others, and K's rows are half
+// a line.  512 heads of 128 .. 8192 tokens cut to 2048: 280 MB kept, about 370 MB of lines, in 72 us.
 #include "splitzip_kv4_internal.h"
 
 namespace sz {
