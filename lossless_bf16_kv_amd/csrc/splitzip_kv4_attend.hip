@@ -258,7 +258,7 @@ __device__ __forceinline__ void take_pair(const uint8_t *slot, uint32_t lane, Pa
                      "ds_read_b128 %0, %8\n"
                      "ds_read_b128 %1, %8 offset:1024\n"
                      "ds_read_b128 %2, %8 offset:2048\n"
-                     "ds_read_b128 %3, %8 offset:3072\n"
+                     "ds_read_b128 %3, %8 offset:0xc00\n"
                      "ds_read_u8 %4, %9 offset:4096\n"
                      "ds_read_u8 %5, %9 offset:4160\n"
                      "ds_read_b32 %6, %10 offset:4224\n"
@@ -278,7 +278,7 @@ __device__ __forceinline__ void take_pair(const uint8_t *slot, uint32_t lane, Pa
                      "ds_read_b128 %0, %12\n"
                      "ds_read_b128 %1, %12 offset:1024\n"
                      "ds_read_b128 %2, %12 offset:2048\n"
-                     "ds_read_b128 %3, %12 offset:3072\n"
+                     "ds_read_b128 %3, %12 offset:0xc00\n"
                      "ds_read_b128 %4, %12 offset:4096\n"
                      "ds_read_b128 %5, %12 offset:5120\n"
                      "ds_read_b128 %6, %12 offset:6144\n"

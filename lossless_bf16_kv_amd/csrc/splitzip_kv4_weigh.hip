@@ -123,7 +123,7 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
                      "ds_read_b128 %0, %9\n"
                      "ds_read_b128 %1, %9 offset:1024\n"
                      "ds_read_b128 %2, %9 offset:2048\n"
-                     "ds_read_b128 %3, %9 offset:3072\n"
+                     "ds_read_b128 %3, %9 offset:0xc00\n"
                      "ds_read_u8 %4, %10 offset:4096\n"
                      "ds_read_u8 %5, %10 offset:4160\n"
                      "ds_read_u8 %6, %10 offset:4224\n"
@@ -145,7 +145,7 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
                      "ds_read_b128 %0, %13\n"
                      "ds_read_b128 %1, %13 offset:1024\n"
                      "ds_read_b128 %2, %13 offset:2048\n"
-                     "ds_read_b128 %3, %13 offset:3072\n"
+                     "ds_read_b128 %3, %13 offset:0xc00\n"
                      "ds_read_b128 %4, %13 offset:4096\n"
                      "ds_read_b128 %5, %13 offset:5120\n"
                      "ds_read_b128 %6, %13 offset:6144\n"
