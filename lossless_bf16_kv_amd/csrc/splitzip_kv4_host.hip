@@ -72,8 +72,9 @@ int check_batch(const splitzip_kv4_batch *b, const Cache &c, bool rows, Batch *o
 {
     KV4_REQUIRE(b, "batch is null");
     KV4_REQUIRE(b->n_seqs >= 0 && b->total >= 0 && b->total < INT32_MAX, "negative or too large batch");
-    KV4_REQUIRE(b->table_width >= 0 && ((int64_t)b->table_width << c.page_shift) <= INT32_MAX - 4096,
-                "table_width is negative or holds 2^31 tokens or more");
+    // kernels count up to 32768 tokens past a sequence's last in 32 bits
+    KV4_REQUIRE(b->table_width >= 0 && ((int64_t)b->table_width << c.page_shift) <= INT32_MAX - 65536,
+                "table_width is negative or holds 2^31 - 65536 tokens or more");
     KV4_REQUIRE(b->n_seqs == 0 || (b->lens && (b->table || b->table_width == 0)), "lens or table is null");
     KV4_REQUIRE(b->n_seqs <= 1 || b->table_stride >= b->table_width, "table_stride is below table_width");
     KV4_REQUIRE(!rows || b->cu_seqlens || b->total == b->n_seqs, "without cu_seqlens there is one row a sequence");
