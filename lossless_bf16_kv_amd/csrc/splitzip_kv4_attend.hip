@@ -366,28 +366,34 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : Cols == 2 ? 2 : T == SPLITZI
         const int v0 = first + 2 * wave;
         auto group = [&](int v) { return v < last ? groups.at(v) : -1; };
         const int turns = v0 < last ? (last - v0 + 7) >> 3 : 0;
-        uint32_t missing = 0;                    // bits 2 i, 2 i + 1: the groups of slot i have no page
+        // a turn's groups; -1: none, or on a bad page
+        struct Two {
+            int a, b;
+        };
         auto send = [&](int i) {
-            const int v = v0 + 8 * i, slot = i & 1;
+            const int v = v0 + 8 * i;
             const int pa = pages_a.at(a.c, a.b, at.s, groups, v0, 8, last, i);
             const int pb = pages_b.at(a.c, a.b, at.s, groups, v0 + 1, 8, last, i);
-            missing = (missing & ~(3u << (2 * slot))) | ((pa < 0 ? 1u : 0u) | (pb < 0 ? 2u : 0u)) << (2 * slot);
-            send_pair<D>(a.c, pa, pb, at.head, group(v), group(v + 1), lane, sh[wave].ring.slot[slot]);
+            const int ga = group(v), gb = group(v + 1);
+            send_pair<D>(a.c, pa, pb, at.head, ga, gb, lane, sh[wave].ring.slot[i & 1]);
+            return Two{ga | pa >> 31, gb | pb >> 31};
         };
+        Two now = {-1, -1}, then = {-1, -1};
         if (turns > 0)
-            send(0);
+            now = send(0);
         if (turns > 1)
-            send(1);
+            then = send(1);
         for (int n = 0; n < turns; ++n) {
             Pair<D> cur;
             if (n + 1 < turns)
                 take_pair<D, Ring<D>::kLoads>(sh[wave].ring.slot[n & 1], lane, cur);
             else
                 take_pair<D, 0>(sh[wave].ring.slot[n & 1], lane, cur);
-            cur.ga = missing >> (2 * (n & 1)) & 1 ? -1 : group(v0 + 8 * n);
-            cur.gb = missing >> (2 * (n & 1)) & 2 ? -1 : group(v0 + 8 * n + 1);
+            cur.ga = now.a;
+            cur.gb = now.b;
+            now = then;
             if (n + 2 < turns)
-                send(n + 2);
+                then = send(n + 2);
             f32x4 sa[Cols], sb[Cols];
 #pragma unroll
             for (int c = 0; c < Cols; ++c)
@@ -403,7 +409,7 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : Cols == 2 ? 2 : T == SPLITZI
                         sb[c] = mfma(fb, qf[c][h][st], sb[c]);
                     }
             }
-            const bool whole = cur.ga >= 0 && cur.gb >= 0 && mask.all(cur.ga, q_lo, q_hi) && mask.all(cur.gb, q_lo, q_hi);
+            const bool whole = (cur.ga >= 0) & (cur.gb >= 0) & mask.all(cur.ga, q_lo, q_hi) & mask.all(cur.gb, q_lo, q_hi);
             const int ja = 16 * cur.ga + 4 * quad, jb = 16 * cur.gb + 4 * quad;
             bf16x8 pf[Cols][kHalves];
 #pragma unroll
@@ -697,7 +703,7 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                     g[n] = v + n < last ? groups.at(v + n) : -1;
                     if (notes != 0 && (__builtin_amdgcn_readfirstlane(st.note[2 * tile + n]) & 1))
                         g[n] = -1;
-                    whole = whole && g[n] >= 0 && mask.all(g[n], q_lo, q_hi);
+                    whole = whole & (g[n] >= 0) & mask.all(g[n], q_lo, q_hi);
                 }
                 // scores of 32 tokens a tile, ahead of the other wave's exponentials: the matrix unit idles less
                 // (457 -> 417 us for 4096 queries of 32 heads on 8192 tokens, with the probabilities made before the

@@ -111,7 +111,7 @@ struct Pages {
     }
 };
 
-// Which tokens queries lo .. hi see.
+// Which tokens queries lo .. hi see.  No short circuits: branches would cost more than the comparisons.
 struct Mask {
     int window, sinks;
     __device__ bool sees(int query, int j) const
@@ -119,10 +119,10 @@ struct Mask {
         return (j <= query) & ((j < sinks) | (window == 0) | (j > query - window));
     }
     // every query of lo .. hi sees every token of group g
-    __device__ bool all(int g, int lo, int hi) const
+    __device__ int all(int g, int lo, int hi) const
     {
         const int j = 16 * g;
-        return j + 15 <= lo && (j + 15 < sinks || window == 0 || j > hi - window);
+        return (j + 15 <= lo) & ((j + 15 < sinks) | (window == 0) | (j > hi - window));
     }
 };
 
