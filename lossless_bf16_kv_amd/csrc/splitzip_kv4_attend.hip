@@ -14,13 +14,15 @@
 // Two kernels.  few_rows: up to 16 or 32 rows a sequence and KV head (a decode step, a few drafts).
 // Each wave takes pairs of groups of its own, has the codes of the next two pairs on their way to LDS
 // while it works on this one, and waits for no other wave until their results are joined.  32 decode
-// steps at 32768 tokens (64 heads on 8 of 128 channels): 1.14 GB in 217 us, 5.3 TB/s, 75 % of what
-// reading alone reaches; the same loads into registers: 229 us.  Past that the instructions bound it:
-// 223 vector and 16 matrix ones for 32 tokens, 96 of them conversions.
+// steps at 32768 tokens (64 heads on 8 of 128 channels): 1.14 GB in 218 us, 5.2 TB/s, 74 % of what
+// reading alone reaches; the same loads into registers: 229 us.  Waves wait for memory 17 % of their
+// time; 223 vector (96 conversions and transpositions) and 16 matrix instructions for 32 tokens keep
+// those units busy 49 and 14 % of it.  More waves, priorities and 15 % fewer scalar instructions did
+// not change the time.
 //
 // many_rows: 64, 128 or 256 rows a workgroup (long drafts, prefill chunks), which share the conversion
-// of V.  4096 queries of 32 heads on 8192 tokens: 412 GFLOP in 417 us, 0.99 PFLOP/s, three quarters of
-// a large bf16 matrix product's rate here; matrix unit and vector unit are each busy about half of the
+// of V.  4096 queries of 32 heads on 8192 tokens: 412 GFLOP in 414 us, 1.0 PFLOP/s, three quarters of
+// a large bf16 matrix product's rate here; the matrix unit is busy 43 % and the vector unit 56 % of the
 // time, and the rest is what two waves on a unit leave open.  Before: 16-row products with K in LDS as
 // bf16, 1409 us (LDS reads as long as the products); 32-row products and K's codes in LDS, 680; two
 // tiles at a time, 571; heads fastest, so that a head's tiles share an L2, 457.
@@ -983,7 +985,7 @@ void attend_d(const AttendArgs &a, int dtype, hipStream_t s)
 }  // namespace
 
 // Few rows wait for nobody, and waste no products on rows that are not there: drafts of 12 to 24 rows take
-// 35 us by few_rows and 79 us in a tile of 64, decode steps of 8 rows 41 and 92 us.  More rows pay for a
+// 34 us by few_rows and 79 us in a tile of 64, decode steps of 8 rows 41 and 92 us.  More rows pay for a
 // shared conversion: 16384 rows 672 us by 64, 511 by 128, 419 by 256.  At 256 channels 32 rows by few_rows
 // and 256 by many_rows would not leave room for two waves' registers.
 int attend_rows(int head_dim, int64_t rows)
