@@ -127,6 +127,7 @@ int splitzip_kv4_attend_workspace(const splitzip_kv4_cache *cache, const splitzi
  * query sees of scale q.k, times v; lse f32 [total][q_heads] (optional) = the logarithm of the
  * sum of exp(scale q.k).  A query that sees nothing, or belongs to no sequence, gets out = 0 and
  * lse = -infinity.
+ * Sums are held in 32 bits: out is finite where sum exp(s - max s) |v| over those tokens is below 2^128.
  */
 int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
                         const splitzip_kv4_queries *queries, void *out, float *lse, void *workspace,

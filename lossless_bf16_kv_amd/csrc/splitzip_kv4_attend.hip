@@ -3,10 +3,11 @@
 //   s_ij = scale q_i . k_j over the tokens j that query i sees
 //   o_i = sum_j exp(s_ij) v_j / sum_j exp(s_ij),  lse_i = log sum_j exp(s_ij)
 //
-// in one pass over the tokens: with x = s log2(e) and any reference m_i >= max x - 8, keep
+// in one pass over the tokens: with x = s log2(e) and any reference m_i >= max x, keep
 // l = sum 2^(x - m) and O = sum 2^(x - m) v, in 32 bits; where the reference has to grow, l and O
-// are multiplied by 2^(m_old - m_new).  Growing it only when a score passes it by 2^8 leaves the
-// result unchanged and the multiplications rare.
+// are multiplied by 2^(m_old - m_new).  It grows to 8 above the score that passed it, which makes the
+// multiplications rare.  No factor of v is above 1: O leaves 32 bits only where sum 2^(x - max x) |v|
+// does (v goes up to 6 * 2^125).
 //
 // Rows are pairs of a query and a head of the group (row = query * group + head): the heads of a
 // group share K and V, so they fill the 16 columns of a matrix instruction together.
@@ -430,8 +431,8 @@ __global__ __launch_bounds__(kLanes, D == 256 ? 1 : Cols == 2 ? 2 : T == SPLITZI
                     }
                 }
                 const float top = quad_max(max_of(x)) * scale.by;
-                if (__any(top > m[c] + 8.0f)) {
-                    const float grown = fmaxf(m[c], top);
+                if (__any(top > m[c])) {
+                    const float grown = fmaxf(m[c], top + 8.0f);
                     const float f = grown == -INFINITY ? 1.0f : exp2_fast(m[c] - grown);
                     m[c] = grown;
                     l[c] *= f;
@@ -762,8 +763,8 @@ __global__ __launch_bounds__(64 * kWaves, D == 256 ? 1 : 2) void many_rows(Atten
                     top = fmaxf(top, max_of(y));
                 }
                 top = half_max(top) * scale.by;
-                if (__any(top > m + 8.0f)) {
-                    const float grown = fmaxf(m, top);
+                if (__any(top > m)) {
+                    const float grown = fmaxf(m, top + 8.0f);
                     const float f = grown == -INFINITY ? 1.0f : exp2_fast(m - grown);
                     m = grown;
                     l *= f;

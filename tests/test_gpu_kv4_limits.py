@@ -1,0 +1,39 @@
+"""GPU tests of the 4-bit KV cache at the ends of its range, against the 64-bit implementations of
+tests/kv4_reference.py: the largest values that the format holds."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+import kv4_reference as ref
+from test_gpu_kv4 import BF16, Setup
+
+pytestmark = pytest.mark.gpu
+
+
+# queries of the two sequences: with a group of 4, 4, 20, 52, 100 and 300 rows of the first
+@pytest.mark.parametrize("count", [1, 5, 13, 25, 75])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_largest_values(d, count):
+    # Base-2 scores: 0 for the first 32 tokens, 6 for one 128 tokens on (which the same wave meets later), -192 for
+    # the others.  That one holds the format's largest values: times 2^6 they leave 32 bits, times their
+    # share of the softmax, 2/3, they do not.
+    s = Setup([300, 700], [count, 1], heads=1, d=d, page=32, seed=d)
+    n = len(s.k)
+    k, v = torch.full((n, 1, d), 0.0), s.v.float()
+    for first, length in ((0, 300), (300, 700)):
+        k[first:first + length, 0, 0] = -192.0
+        k[first:first + 32, 0, 0] = 0.0
+        k[first + 130, 0, 0] = 6.0
+        v[first + 130, 0] = 6 * 2.0 ** 125 * torch.where(torch.arange(d) % 3 == 0, -1.0, 1.0)
+    s.cache.append(k.cuda(), v.cuda(), s.table, s.lens, s.fill_cu)
+    q = torch.zeros(s.total, 4, d, dtype=BF16)
+    q[:, :, 0] = 1.0
+    scale = math.log(2)
+    out, lse = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, scale=scale)
+    eo, to, el, tl = ref.attend(ref.Cache(s.cache), q.double(), s.rows(), s.lens_l, s.counts, scale, None, 0, BF16)
+    assert out.isfinite().all()
+    assert ((out.cpu().double() - eo).abs() <= to).all()
+    assert ((lse.cpu().double() - el).abs() <= tl).all()
