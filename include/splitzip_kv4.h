@@ -149,7 +149,8 @@ int splitzip_kv4_weigh(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
  * counts as the lowest weight), each KV head for itself.  What is kept moves, in token order,
  * with its weights, to tokens 0 .. of the pages of out_table [n_seqs][>= budget / page_size
  * rounded up], which must share no page with `table`.  out_lens i32 [n_seqs], apart from
- * batch->lens; kept i32 [n_seqs][kv_heads][budget], -1 behind the last.  batch->cu_seqlens, total, max_q are not read.
+ * batch->lens; kept i32 [n_seqs][kv_heads][budget], -1 behind the last.  budget is below 2^31 - 65536.
+ * batch->cu_seqlens, total, max_q are not read.
  */
 int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
                        const int32_t *out_table, int64_t out_table_stride, int32_t out_table_width,

@@ -287,7 +287,9 @@ int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
                 "out_table_stride is below out_table_width");
     // lengths are read while new ones are written
     KV4_REQUIRE(out_lens + a.b.n_seqs <= a.b.lens || a.b.lens + a.b.n_seqs <= out_lens, "out_lens must not overlap lens");
-    KV4_REQUIRE((int64_t)a.b.n_seqs * a.c.heads * ceil_div(budget, 16) < INT32_MAX, "too many tokens to keep");
+    // kernels count up to 1024 tokens past the budget in 32 bits
+    KV4_REQUIRE(budget <= INT32_MAX - 65536 && (int64_t)a.b.n_seqs * a.c.heads * ceil_div(budget, 16) < INT32_MAX,
+                "too many tokens to keep");
     a.out_table = out_table;
     a.out_stride = out_table_stride;
     a.out_width = out_table_width;

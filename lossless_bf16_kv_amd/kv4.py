@@ -270,6 +270,8 @@ class KV4Cache:
         -> (out_lens int32 [seqs], kept int32 [seqs, kv_heads, budget], -1 behind the last)."""
         if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
             raise ValueError("budget must be at least 1 and hold sinks and recent")
+        if budget > _BIG - 65536:
+            raise ValueError("budget must be below 2^31 - 65536")
         b = self._batch(table, lens, None, table.shape[0], None, max_len)
         if out_table.dim() != 2 or out_table.shape[0] != table.shape[0]:
             raise ValueError("out_table must be [seqs, pages]")
