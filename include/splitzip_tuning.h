@@ -9,6 +9,7 @@
 #define SPLITZIP_TUNING_H
 
 #include "splitzip.h"
+#include "splitzip_kv4.h"
 
 #ifdef __cplusplus
 extern "C" {
@@ -102,6 +103,19 @@ int splitzip_set_stage_tiles(splitzip_codec *codec, uint32_t min_tiles);
  * Applies to calls that start after it returns.
  */
 int splitzip_set_private_overflow(splitzip_codec *codec, uint64_t max_bytes);
+
+/* ---- launches of the 4-bit KV cache (splitzip_kv4.h) ---- */
+
+#define SPLITZIP_KV4_EVICT 2
+
+/*
+ * What a call with these arguments launches, one after the other: workgroups and threads of a
+ * workgroup, 0 where there is no such launch.  Nothing is launched and no pointer but the structs'
+ * own is followed.  budget: of an eviction.
+ */
+int splitzip_kv4_launches(int32_t op, const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
+                          const splitzip_kv4_queries *queries, int32_t budget, uint64_t workgroups[2],
+                          uint32_t threads[2]);
 
 /* ---- per-kernel timing (for benchmarks and profilers: the codec throughput measurement
  *      of README "Quick Start") ---- */

@@ -22,12 +22,12 @@ namespace sz {
 namespace kv4 {
 namespace {
 
-constexpr int kChoose = 1024;
+constexpr int kChoose = kChooseThreads;
 constexpr int kWaves = kChoose / 64;
 constexpr int kUnits = 8;             // runs of 256 tokens a wave holds: 32 keys a lane
 constexpr int kCopies = 32;           // of each count: lanes of one wave meet only in pairs
-constexpr int kMove = 256;
-constexpr int kTokens = 128;          // of a workgroup of move_kernel
+constexpr int kMove = kMoveThreads;
+constexpr int kTokens = kMoveTokens;  // a workgroup of move_kernel at a time
 
 // Larger weight, larger key; -0 as 0, NaN the smallest.  0 is left for "no token", the largest value
 // for tokens that stay whatever they weigh.
@@ -264,133 +264,138 @@ __global__ __launch_bounds__(kMove) void move_kernel(EvictArgs a)
     // token offsets in the buffers, page * heads * page_size and so on; -1: no page; and the place in the page
     __shared__ int64_t sh_from[kTokens], sh_to[kTokens];
     __shared__ int sh_from_in[kTokens], sh_to_in[kTokens];
-    const int turns = (a.budget + kTokens - 1) / kTokens;
-    const int turn = blockIdx.x % turns;
-    const uint32_t pair = blockIdx.x / turns;
+    const uint32_t pair = blockIdx.x / a.turns;
     const int head = pair % a.c.heads, s = pair / a.c.heads;
-    const int tid = threadIdx.x;
     Batch bt = a.b;
     bt.cu = nullptr;
     const int64_t cap = (int64_t)a.out_width << a.c.page_shift;
     const int keep = (int)min((int64_t)min(wave_sequence(a.c, bt, s).len, a.budget), cap);
-    const int to0 = turn * kTokens;
-    if (to0 >= keep)
-        return;
-    const int n = min(kTokens, keep - to0);
-    if (tid < kTokens) {
-        const int mask = (1 << a.c.page_shift) - 1;
-        int64_t from = -1, to = -1;
-        if (tid < n) {
-            const int j = a.kept[((int64_t)s * a.c.heads + head) * a.budget + to0 + tid];
-            const int out_page = a.out_table[(int64_t)s * a.out_stride + ((to0 + tid) >> a.c.page_shift)];
-            const int page = page_of(a.c, a.b, s, j);
-            sh_from_in[tid] = j & mask;
-            sh_to_in[tid] = (to0 + tid) & mask;
-            if (page >= 0)
-                from = ((int64_t)page * a.c.heads + head) << a.c.page_shift;
-            if (out_page >= 0 && out_page < a.c.num_pages)
-                to = ((int64_t)out_page * a.c.heads + head) << a.c.page_shift;
-            else
-                flag(a.c, SPLITZIP_KV4_BAD_PAGE);
+    for (int64_t at = (int64_t)(blockIdx.x % a.turns) * kTokens; at < keep; at += (int64_t)a.turns * kTokens) {
+        const int to0 = (int)at;
+        // The empty asm keeps the compiler from holding a turn's offsets over the others, of which there is
+        // hardly ever one: 50 registers for 78 (D = 128), 512 ragged heads 4 us less.
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int n = min(kTokens, keep - to0);
+        if (tid < kTokens) {
+            const int mask = (1 << a.c.page_shift) - 1;
+            int64_t from = -1, to = -1;
+            if (tid < n) {
+                const int j = a.kept[((int64_t)s * a.c.heads + head) * a.budget + to0 + tid];
+                const int out_page = a.out_table[(int64_t)s * a.out_stride + ((to0 + tid) >> a.c.page_shift)];
+                const int page = page_of(a.c, a.b, s, j);
+                sh_from_in[tid] = j & mask;
+                sh_to_in[tid] = (to0 + tid) & mask;
+                if (page >= 0)
+                    from = ((int64_t)page * a.c.heads + head) << a.c.page_shift;
+                if (out_page >= 0 && out_page < a.c.num_pages)
+                    to = ((int64_t)out_page * a.c.heads + head) << a.c.page_shift;
+                else
+                    flag(a.c, SPLITZIP_KV4_BAD_PAGE);
+            }
+            sh_from[tid] = from;
+            sh_to[tid] = to;
         }
-        sh_from[tid] = from;
-        sh_to[tid] = to;
-    }
-    __syncthreads();
+        __syncthreads();
 
-    uint4 k[kK];
+        uint4 k[kK];
 #pragma unroll
-    for (int i = 0; i < kK; ++i) {
-        const int t = (i * kMove + tid) / kPieces, p = tid % kPieces;
-        const int64_t f = sh_from[t];
-        k[i] = f < 0 ? make_uint4(0, 0, 0, 0) : *(const uint4 *)(a.c.k_codes + (f + sh_from_in[t]) * (D / 2) + 16 * p);
-    }
-    run_t v[kV][4];
-#pragma unroll
-    for (int i = 0; i < kV; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int t = (i * kMove + tid) / 16 * 4 + e, run = tid % 16;
+        for (int i = 0; i < kK; ++i) {
+            const int t = (i * kMove + tid) / kPieces, p = tid % kPieces;
             const int64_t f = sh_from[t];
-            const int in = sh_from_in[t];
-            v[i][e] = f < 0 ? 0 : *(const run_t *)(a.c.v_codes + f * (D / 2) + (in >> 2) * (2 * D) + run * (D / 8) +
-                                                   (in & 3) * (D / 32));
+            k[i] = f < 0 ? make_uint4(0, 0, 0, 0) : *(const uint4 *)(a.c.k_codes + (f + sh_from_in[t]) * (D / 2) + 16 * p);
         }
-    uint8_t vs[kS][4];
+        run_t v[kV][4];
 #pragma unroll
-    for (int i = 0; i < kS; ++i)
+        for (int i = 0; i < kV; ++i)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int u = i * kMove + tid, t = u % (kTokens / 4) * 4 + e, block = u / (kTokens / 4);
-            const int64_t f = block < kBlocks ? sh_from[t] : -1;
-            vs[i][e] = f < 0 ? 0 : a.c.v_scales[f * kBlocks + ((int64_t)block << a.c.page_shift) + sh_from_in[t]];
+            for (int e = 0; e < 4; ++e) {
+                const int t = (i * kMove + tid) / 16 * 4 + e, run = tid % 16;
+                const int64_t f = sh_from[t];
+                const int in = sh_from_in[t];
+                v[i][e] = f < 0 ? 0 : *(const run_t *)(a.c.v_codes + f * (D / 2) + (in >> 2) * (2 * D) + run * (D / 8) +
+                                                       (in & 3) * (D / 32));
+            }
+        uint8_t vs[kS][4];
+#pragma unroll
+        for (int i = 0; i < kS; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int u = i * kMove + tid, t = u % (kTokens / 4) * 4 + e, block = u / (kTokens / 4);
+                const int64_t f = block < kBlocks ? sh_from[t] : -1;
+                vs[i][e] = f < 0 ? 0 : a.c.v_scales[f * kBlocks + ((int64_t)block << a.c.page_shift) + sh_from_in[t]];
+            }
+        run_t ks = 0;                                   // D / 32 bytes as well
+        float w = 0.0f;
+        if (tid < n && sh_from[tid] >= 0) {
+            ks = *(const run_t *)(a.c.k_scales + (sh_from[tid] + sh_from_in[tid]) * kBlocks);
+            w = a.c.weights[sh_from[tid] + sh_from_in[tid]];
         }
-    run_t ks = 0;                                   // D / 32 bytes as well
-    float w = 0.0f;
-    if (tid < n && sh_from[tid] >= 0) {
-        ks = *(const run_t *)(a.c.k_scales + (sh_from[tid] + sh_from_in[tid]) * kBlocks);
-        w = a.c.weights[sh_from[tid] + sh_from_in[tid]];
-    }
 
 #pragma unroll
-    for (int i = 0; i < kK; ++i) {
-        const int t = (i * kMove + tid) / kPieces, p = tid % kPieces;
-        const int64_t o = sh_to[t];
-        if (o >= 0)
-            *(uint4 *)(a.c.k_codes + (o + sh_to_in[t]) * (D / 2) + 16 * p) = k[i];
-    }
-    // four tokens lie in one page on both sides of their stores: pages hold multiples of 16
-#pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const int t = (i * kMove + tid) / 16 * 4, run = tid % 16;
-        const int64_t o = sh_to[t];
-        if (o < 0)
-            continue;
-        run_t *to = (run_t *)(a.c.v_codes + o * (D / 2) + (sh_to_in[t] >> 2) * (2 * D) + run * (D / 8));
-        if (t + 3 < n) {
-            typedef run_t four __attribute__((ext_vector_type(4)));
-            *(four *)to = four{v[i][0], v[i][1], v[i][2], v[i][3]};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t + e < n)
-                    to[e] = v[i][e];
+        for (int i = 0; i < kK; ++i) {
+            const int t = (i * kMove + tid) / kPieces, p = tid % kPieces;
+            const int64_t o = sh_to[t];
+            if (o >= 0)
+                *(uint4 *)(a.c.k_codes + (o + sh_to_in[t]) * (D / 2) + 16 * p) = k[i];
         }
-    }
+        // four tokens lie in one page on both sides of their stores: pages hold multiples of 16
 #pragma unroll
-    for (int i = 0; i < kS; ++i) {
-        const int u = i * kMove + tid, t = u % (kTokens / 4) * 4, block = u / (kTokens / 4);
-        const int64_t o = block < kBlocks ? sh_to[t] : -1;
-        if (o < 0)
-            continue;
-        uint8_t *to = a.c.v_scales + o * kBlocks + ((int64_t)block << a.c.page_shift) + sh_to_in[t];
-        if (t + 3 < n) {
-            *(uint32_t *)to = vs[i][0] | (uint32_t)vs[i][1] << 8 | (uint32_t)vs[i][2] << 16 | (uint32_t)vs[i][3] << 24;
-        } else {
+        for (int i = 0; i < kV; ++i) {
+            const int t = (i * kMove + tid) / 16 * 4, run = tid % 16;
+            const int64_t o = sh_to[t];
+            if (o < 0)
+                continue;
+            run_t *to = (run_t *)(a.c.v_codes + o * (D / 2) + (sh_to_in[t] >> 2) * (2 * D) + run * (D / 8));
+            if (t + 3 < n) {
+                typedef run_t four __attribute__((ext_vector_type(4)));
+                *(four *)to = four{v[i][0], v[i][1], v[i][2], v[i][3]};
+            } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (t + e < n)
-                    to[e] = vs[i][e];
+                for (int e = 0; e < 4; ++e)
+                    if (t + e < n)
+                        to[e] = v[i][e];
+            }
         }
-    }
-    if (tid < n && sh_to[tid] >= 0) {
-        *(run_t *)(a.c.k_scales + (sh_to[tid] + sh_to_in[tid]) * kBlocks) = ks;
-        a.c.weights[sh_to[tid] + sh_to_in[tid]] = w;
+#pragma unroll
+        for (int i = 0; i < kS; ++i) {
+            const int u = i * kMove + tid, t = u % (kTokens / 4) * 4, block = u / (kTokens / 4);
+            const int64_t o = block < kBlocks ? sh_to[t] : -1;
+            if (o < 0)
+                continue;
+            uint8_t *to = a.c.v_scales + o * kBlocks + ((int64_t)block << a.c.page_shift) + sh_to_in[t];
+            if (t + 3 < n) {
+                *(uint32_t *)to = vs[i][0] | (uint32_t)vs[i][1] << 8 | (uint32_t)vs[i][2] << 16 | (uint32_t)vs[i][3] << 24;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (t + e < n)
+                        to[e] = vs[i][e];
+            }
+        }
+        if (tid < n && sh_to[tid] >= 0) {
+            *(run_t *)(a.c.k_scales + (sh_to[tid] + sh_to_in[tid]) * kBlocks) = ks;
+            a.c.weights[sh_to[tid] + sh_to_in[tid]] = w;
+        }
+        __syncthreads();                            // the places are free again
     }
 }
 
 }  // namespace
 
-void launch_evict(const EvictArgs &a, int head_dim, hipStream_t s)
+hipError_t launch_evict(const EvictArgs &a, int head_dim, hipStream_t s)
 {
     choose_kernel<<<(unsigned)(a.b.n_seqs * a.c.heads), kChoose, 0, s>>>(a);
-    const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * ((a.budget + kTokens - 1) / kTokens));
+    if (const hipError_t e = hipGetLastError())
+        return e;                               // move_kernel would read kept tokens that nobody wrote
+    const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.turns);
     if (head_dim == 64)
         move_kernel<64><<<grid, kMove, 0, s>>>(a);
     else if (head_dim == 128)
         move_kernel<128><<<grid, kMove, 0, s>>>(a);
     else
         move_kernel<256><<<grid, kMove, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace kv4

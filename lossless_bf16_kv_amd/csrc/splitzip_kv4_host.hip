@@ -1,6 +1,7 @@
 // splitzip_kv4_host.hip -- entry points of the 4-bit KV cache (include/splitzip_kv4.h): argument
 // checks and the choice of launches.
 #include "splitzip_kv4_internal.h"
+#include "splitzip_tuning.h"
 
 #include <algorithm>
 #include <cmath>
@@ -43,9 +44,8 @@ struct Device {
         snprintf(text, sizeof text, "4-bit cache launch: %s", hipGetErrorString(e));
         return report(e == hipErrorOutOfMemory ? SPLITZIP_E_NOMEM : SPLITZIP_E_DEVICE, text);
     }
-    static int launched()
+    static int launched(hipError_t e = hipGetLastError())
     {
-        const hipError_t e = hipGetLastError();
         return e == hipSuccess ? SPLITZIP_OK : failed(e);
     }
 };
@@ -136,6 +136,16 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
 uint64_t workspace_of(const AttendArgs &a, int head_dim)
 {
     return a.splits == 1 ? 0 : (uint64_t)a.splits * a.b.total * a.q_heads * (head_dim + 2) * 4;
+}
+
+// Launches of an evict call.  A sequence and head's workgroups of move_kernel take its kept tokens in
+// turn, so a launch that would be too large has fewer of them.
+int plan_evict(const Batch &b, const Cache &c, int32_t budget, EvictArgs *a)
+{
+    const int64_t pairs = (int64_t)b.n_seqs * c.heads;
+    KV4_REQUIRE(pairs <= kMostThreads / kChooseThreads, "too many sequences and heads");
+    a->turns = (int32_t)std::min(ceil_div(budget, kMoveTokens), kMostThreads / kMoveThreads / std::max<int64_t>(1, pairs));
+    return SPLITZIP_OK;
 }
 
 }  // namespace
@@ -290,6 +300,8 @@ int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
     // kernels count up to 1024 tokens past the budget in 32 bits
     KV4_REQUIRE(budget <= INT32_MAX - 65536 && (int64_t)a.b.n_seqs * a.c.heads * ceil_div(budget, 16) < INT32_MAX,
                 "too many tokens to keep");
+    if (int e = plan_evict(a.b, a.c, budget, &a))
+        return e;
     a.out_table = out_table;
     a.out_stride = out_table_stride;
     a.out_width = out_table_width;
@@ -301,8 +313,30 @@ int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
     Device d(cache->device);
     if (d.status)
         return d.status;
-    launch_evict(a, cache->head_dim, static_cast<hipStream_t>(stream));
-    return Device::launched();
+    return Device::launched(launch_evict(a, cache->head_dim, static_cast<hipStream_t>(stream)));
+}
+
+int splitzip_kv4_launches(int32_t op, const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
+                          const splitzip_kv4_queries *queries, int32_t budget, uint64_t workgroups[2], uint32_t threads[2])
+{
+    KV4_REQUIRE(op == SPLITZIP_KV4_EVICT, "no such operator");
+    KV4_REQUIRE(workgroups && threads, "workgroups or threads is null");
+    for (int i = 0; i < 2; ++i)
+        workgroups[i] = threads[i] = 0;
+    EvictArgs a;
+    if (int e = check_cache(cache, &a.c))
+        return e;
+    if (int e = check_batch(batch, a.c, false, &a.b))
+        return e;
+    if (a.b.n_seqs == 0)
+        return SPLITZIP_OK;
+    if (int e = plan_evict(a.b, a.c, budget, &a))
+        return e;
+    workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads;
+    threads[0] = kChooseThreads;
+    workgroups[1] = workgroups[0] * a.turns;
+    threads[1] = kMoveThreads;
+    return SPLITZIP_OK;
 }
 
 }  // extern "C"

@@ -65,14 +65,19 @@ struct EvictArgs {
     int32_t out_width;
     int32_t budget, sinks, recent;
     int32_t *out_lens, *kept;
+    int32_t turns;           // workgroups of move_kernel a sequence and head
 };
+
+// HIP launches fewer than 2^32 threads at a time.
+constexpr int64_t kMostThreads = UINT32_MAX;
+constexpr int kChooseThreads = 1024, kMoveThreads = 256, kMoveTokens = 128;
 
 void launch_append(const AppendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_read(const ReadArgs &a, int head_dim, int dtype, hipStream_t s);
 int attend_rows(int head_dim, int64_t rows);   // rows of a workgroup for this many rows a sequence
 void launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_weigh(const AttendArgs &a, int head_dim, int dtype, int max_q, int max_len, hipStream_t s);
-void launch_evict(const EvictArgs &a, int head_dim, hipStream_t s);
+hipError_t launch_evict(const EvictArgs &a, int head_dim, hipStream_t s);
 
 // ---- device ---------------------------------------------------------------------------------
 #ifdef __HIPCC__

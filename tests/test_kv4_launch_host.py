@@ -2,11 +2,13 @@
 here reaches the GPU."""
 from __future__ import annotations
 
+import ctypes
+
 import pytest
 
 import lossless_bf16_kv_amd as sz
 from lossless_bf16_kv_amd import kv4
-from test_kv4_host import batch, cache, call
+from test_kv4_host import batch, cache, call, queries
 
 MOST = (1 << 31) - 1
 
@@ -28,3 +30,34 @@ def test_evict_budget_past_32_bits_is_not_cut(budget):
     # before anything of the cache is looked at
     with pytest.raises(ValueError, match="budget"):
         kv4.KV4Cache.evict(None, None, None, None, budget)
+
+
+def launches(op, c=None, b=None, q=None, budget=100):
+    """(workgroups, threads) of each launch."""
+    f = kv4._lib().splitzip_kv4_launches
+    f.argtypes = [ctypes.c_int32, *(ctypes.POINTER(t) for t in (kv4.splitzip_kv4_cache, kv4.splitzip_kv4_batch,
+                                                                kv4.splitzip_kv4_queries)), ctypes.c_int32,
+                  ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint32)]
+    groups, threads = (ctypes.c_uint64 * 2)(), (ctypes.c_uint32 * 2)()
+    status = f(op, *(ctypes.byref(x) for x in (c or cache(), b or batch(), q or queries())), budget, groups, threads)
+    assert status == sz.OK, sz.lib().splitzip_last_error().decode()
+    return [(g, t) for g, t in zip(groups, threads) if g]
+
+
+EVICT = 2
+
+
+# HIP launches fewer than 2^32 threads at a time.  A choose launch that fails leaves nothing for the move behind it.
+@pytest.mark.parametrize("seqs,budget", [(1 << 19, 128), (1 << 20, 1), (1 << 21, 16)])
+def test_evict_of_too_many_heads(seqs, budget):
+    refused("evict", "too many sequences and heads", b=batch(n_seqs=seqs, total=seqs), budget=budget, sinks=0, recent=0, lens=1 << 30)
+
+
+@pytest.mark.parametrize("seqs,budget", [(3, 100), ((1 << 19) - 1, 16), (512, 1 << 19), (1, 1 << 30)])
+def test_evict_launches(seqs, budget):
+    choose, move = launches(EVICT, b=batch(n_seqs=seqs, total=seqs), budget=budget)
+    assert choose == (seqs * 8, 1024) and move[1] == 256
+    assert all(g * t < 1 << 32 for g, t in (choose, move))
+    # every token has a workgroup where that fits, and some workgroup takes it in turn where not
+    turns = -(-budget // 128)
+    assert move[0] == seqs * 8 * (turns if seqs * 8 * turns * 256 < 1 << 32 else ((1 << 32) - 1) // 256 // (seqs * 8))
