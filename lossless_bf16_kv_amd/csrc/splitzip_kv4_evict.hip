@@ -272,8 +272,8 @@ __global__ __launch_bounds__(kMove) void move_kernel(EvictArgs a)
     const int keep = (int)min((int64_t)min(wave_sequence(a.c, bt, s).len, a.budget), cap);
     for (int64_t at = (int64_t)(blockIdx.x % a.turns) * kTokens; at < keep; at += (int64_t)a.turns * kTokens) {
         const int to0 = (int)at;
-        // The empty asm keeps the compiler from holding a turn's offsets over the others, of which there is
-        // hardly ever one: 50 registers for 78 (D = 128), 512 ragged heads 4 us less.
+        // The empty asm keeps the compiler from holding a turn's offsets over the others, which only calls with too
+        // small a max_len have: 50 registers for 78 (D = 128), 512 ragged heads 4 us less.
         int tid = threadIdx.x;
         asm volatile("" : "+v"(tid));
         const int n = min(kTokens, keep - to0);

@@ -138,13 +138,15 @@ uint64_t workspace_of(const AttendArgs &a, int head_dim)
     return a.splits == 1 ? 0 : (uint64_t)a.splits * a.b.total * a.q_heads * (head_dim + 2) * 4;
 }
 
-// Launches of an evict call.  A sequence and head's workgroups of move_kernel take its kept tokens in
-// turn, so a launch that would be too large has fewer of them.
-int plan_evict(const Batch &b, const Cache &c, int32_t budget, EvictArgs *a)
+// Launches of an evict call: a workgroup of move_kernel for every 128 tokens that a sequence and head may
+// keep.  A launch that would be too large has fewer, which take tokens in turn.
+int plan_evict(const splitzip_kv4_batch *batch, int32_t budget, EvictArgs *a)
 {
-    const int64_t pairs = (int64_t)b.n_seqs * c.heads;
+    const int64_t pairs = (int64_t)a->b.n_seqs * a->c.heads;
     KV4_REQUIRE(pairs <= kMostThreads / kChooseThreads, "too many sequences and heads");
-    a->turns = (int32_t)std::min(ceil_div(budget, kMoveTokens), kMostThreads / kMoveThreads / std::max<int64_t>(1, pairs));
+    const int64_t longest = std::min<int64_t>(batch->max_len, (int64_t)a->b.table_width << a->c.page_shift);
+    const int64_t turns = ceil_div(std::max<int64_t>(1, std::min<int64_t>(budget, longest)), kMoveTokens);
+    a->turns = (int32_t)std::min(turns, kMostThreads / kMoveThreads / std::max<int64_t>(1, pairs));
     return SPLITZIP_OK;
 }
 
@@ -300,7 +302,7 @@ int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
     // kernels count up to 1024 tokens past the budget in 32 bits
     KV4_REQUIRE(budget <= INT32_MAX - 65536 && (int64_t)a.b.n_seqs * a.c.heads * ceil_div(budget, 16) < INT32_MAX,
                 "too many tokens to keep");
-    if (int e = plan_evict(a.b, a.c, budget, &a))
+    if (int e = plan_evict(batch, budget, &a))
         return e;
     a.out_table = out_table;
     a.out_stride = out_table_stride;
@@ -330,7 +332,7 @@ int splitzip_kv4_launches(int32_t op, const splitzip_kv4_cache *cache, const spl
         return e;
     if (a.b.n_seqs == 0)
         return SPLITZIP_OK;
-    if (int e = plan_evict(a.b, a.c, budget, &a))
+    if (int e = plan_evict(batch, budget, &a))
         return e;
     workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads;
     threads[0] = kChooseThreads;

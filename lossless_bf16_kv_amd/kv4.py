@@ -267,7 +267,8 @@ class KV4Cache:
         """Cuts every sequence to ``budget`` tokens a KV head: its first ``sinks``, its last ``recent`` and
         the tokens of the largest weights between (the lowest first among equals).  They move, in
         token order, to the pages of ``out_table`` (none of which may be in ``table``)
-        -> (out_lens int32 [seqs], kept int32 [seqs, kv_heads, budget], -1 behind the last)."""
+        -> (out_lens int32 [seqs], kept int32 [seqs, kv_heads, budget], -1 behind the last).  ``max_len``
+        (most tokens of a sequence, from the host) only chooses the launch."""
         if budget < 1 or sinks < 0 or recent < 0 or sinks + recent > budget:
             raise ValueError("budget must be at least 1 and hold sinks and recent")
         if budget > _BIG - 65536:

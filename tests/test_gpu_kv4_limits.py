@@ -1,5 +1,6 @@
 """GPU tests of the 4-bit KV cache at the ends of its range, against the 64-bit implementations of
-tests/kv4_reference.py: the largest values that the format holds."""
+tests/kv4_reference.py: the largest values that the format holds,
+hints that say too little."""
 from __future__ import annotations
 
 import math
@@ -8,7 +9,7 @@ import pytest
 import torch
 
 import kv4_reference as ref
-from test_gpu_kv4 import BF16, Setup
+from test_gpu_kv4 import BF16, Setup, check_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +38,11 @@ def test_attend_largest_values(d, count):
     assert out.isfinite().all()
     assert ((out.cpu().double() - eo).abs() <= to).all()
     assert ((lse.cpu().double() - el).abs() <= tl).all()
+
+
+@pytest.mark.parametrize("max_len", [1, 129, 300])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_evict_hint_that_says_too_little(d, max_len):
+    # a move workgroup takes several turns, the last of them short
+    s = Setup([0, 1, 700, 523, 900], [1] * 5, heads=2, d=d, page=32, extra=100, seed=d)
+    check_evict(s, lambda q, n: torch.rand(2, n, generator=s.g), 523, 4, 100, max_len=max_len)

@@ -53,11 +53,24 @@ def test_evict_of_too_many_heads(seqs, budget):
     refused("evict", "too many sequences and heads", b=batch(n_seqs=seqs, total=seqs), budget=budget, sinks=0, recent=0, lens=1 << 30)
 
 
-@pytest.mark.parametrize("seqs,budget", [(3, 100), ((1 << 19) - 1, 16), (512, 1 << 19), (1, 1 << 30)])
+@pytest.mark.parametrize("seqs,budget", [(3, 100), ((1 << 19) - 1, 16), (512, 1 << 19), (1, 64 << 20)])
 def test_evict_launches(seqs, budget):
-    choose, move = launches(EVICT, b=batch(n_seqs=seqs, total=seqs), budget=budget)
+    b = batch(n_seqs=seqs, total=seqs, max_len=MOST, table_width=1 << 20, table_stride=1 << 20)
+    choose, move = launches(EVICT, b=b, budget=budget)
     assert choose == (seqs * 8, 1024) and move[1] == 256
     assert all(g * t < 1 << 32 for g, t in (choose, move))
     # every token has a workgroup where that fits, and some workgroup takes it in turn where not
     turns = -(-budget // 128)
     assert move[0] == seqs * 8 * (turns if seqs * 8 * turns * 256 < 1 << 32 else ((1 << 32) - 1) // 256 // (seqs * 8))
+
+
+@pytest.mark.parametrize("max_len,turns", [(0, 1), (1, 1), (128, 1), (129, 2), (1000, 8), (4096, 8), (MOST, 8)])
+def test_evict_launch_goes_by_the_longest_sequence(max_len, turns):
+    # no sequence keeps more tokens than it has
+    choose, move = launches(EVICT, b=batch(table_width=100, table_stride=100, max_len=max_len), budget=1000)
+    assert choose == (24, 1024) and move == (24 * turns, 256)
+
+
+def test_evict_launch_goes_by_the_table():
+    _, move = launches(EVICT, b=batch(max_len=MOST), budget=1 << 20)          # 5 pages of 64 tokens
+    assert move == (24 * 3, 256)
