@@ -106,12 +106,14 @@ int splitzip_set_private_overflow(splitzip_codec *codec, uint64_t max_bytes);
 
 /* ---- launches of the 4-bit KV cache (splitzip_kv4.h) ---- */
 
+#define SPLITZIP_KV4_ATTEND 0
+#define SPLITZIP_KV4_WEIGH 1
 #define SPLITZIP_KV4_EVICT 2
 
 /*
  * What a call with these arguments launches, one after the other: workgroups and threads of a
  * workgroup, 0 where there is no such launch.  Nothing is launched and no pointer but the structs'
- * own is followed.  budget: of an eviction.
+ * own is followed.  queries: not read for an eviction; budget: for an eviction alone.
  */
 int splitzip_kv4_launches(int32_t op, const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
                           const splitzip_kv4_queries *queries, int32_t budget, uint64_t workgroups[2],

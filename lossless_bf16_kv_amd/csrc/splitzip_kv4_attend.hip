@@ -44,7 +44,7 @@ namespace sz {
 namespace kv4 {
 namespace {
 
-constexpr int kLanes = 256;
+constexpr int kLanes = kJoinThreads;
 
 // Workgroup b -> KV head, row tile, sequence and split, the head fastest: workgroups go to the eight
 // XCDs in turn, so each gets the same share of long and short sequences (with the split fastest one
@@ -953,7 +953,7 @@ __global__ __launch_bounds__(kLanes) void join_kernel(AttendArgs a)
 }
 
 template <int D, int T>
-void attend_dt(const AttendArgs &a, hipStream_t s)
+hipError_t attend_dt(const AttendArgs &a, hipStream_t s)
 {
     const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.tiles * a.splits);
     constexpr int kWaves = D == 256 ? 4 : 8, kLanesMany = 64 * kWaves;
@@ -968,19 +968,18 @@ void attend_dt(const AttendArgs &a, hipStream_t s)
         many_rows<D, T, kWaves, 4><<<grid, kLanesMany, 0, s>>>(a);
     else if constexpr (D < 256)
         many_rows<D, T, kWaves, 8><<<grid, kLanesMany, 0, s>>>(a);
-    if (a.splits > 1) {
-        constexpr int kRows = kLanes / (D / 4);
-        join_kernel<D, T><<<(unsigned)((a.b.total * a.q_heads + kRows - 1) / kRows), kLanes, 0, s>>>(a);
-    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1)
+        return e;
+    const int rows = join_rows(D);
+    join_kernel<D, T><<<(unsigned)((a.b.total * a.q_heads + rows - 1) / rows), kLanes, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 template <int D>
-void attend_d(const AttendArgs &a, int dtype, hipStream_t s)
+hipError_t attend_d(const AttendArgs &a, int dtype, hipStream_t s)
 {
-    if (dtype == SPLITZIP_KV4_BF16)
-        attend_dt<D, SPLITZIP_KV4_BF16>(a, s);
-    else
-        attend_dt<D, SPLITZIP_KV4_FP16>(a, s);
+    return dtype == SPLITZIP_KV4_BF16 ? attend_dt<D, SPLITZIP_KV4_BF16>(a, s) : attend_dt<D, SPLITZIP_KV4_FP16>(a, s);
 }
 
 }  // namespace
@@ -994,11 +993,15 @@ int attend_rows(int head_dim, int64_t rows)
     return rows <= 16 ? 16 : rows <= 32 && head_dim < 256 ? 32 : rows <= 64 ? 64 : rows <= 128 || head_dim == 256 ? 128 : 256;
 }
 
-void launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s)
+int attend_threads(int head_dim, int tile_rows) { return tile_rows <= 32 || head_dim == 256 ? 256 : 512; }
+
+int join_rows(int head_dim) { return kJoinThreads / (head_dim / 4); }
+
+hipError_t launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s)
 {
-    head_dim == 64    ? attend_d<64>(a, dtype, s)
-    : head_dim == 128 ? attend_d<128>(a, dtype, s)
-                      : attend_d<256>(a, dtype, s);
+    return head_dim == 64    ? attend_d<64>(a, dtype, s)
+           : head_dim == 128 ? attend_d<128>(a, dtype, s)
+                             : attend_d<256>(a, dtype, s);
 }
 
 }  // namespace kv4

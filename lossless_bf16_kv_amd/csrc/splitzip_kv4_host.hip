@@ -117,19 +117,42 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
     const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
     a->tile_rows = attend_rows(c->head_dim, rows);
     const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
-    int64_t tiles = ceil_div(rows, a->tile_rows);
-    KV4_REQUIRE(pairs <= INT32_MAX / 4, "too many sequences and heads");
-    tiles = std::min<int64_t>(tiles, std::max<int64_t>(1, INT32_MAX / 4 / std::max<int64_t>(1, pairs)));
+    // workgroups that a launch holds; fewer tiles and splits than there could be take rows and tokens in turn
+    const int64_t most = kMostThreads / attend_threads(c->head_dim, a->tile_rows);
+    KV4_REQUIRE(pairs <= most, "too many sequences and heads");
+    const int64_t tiles = std::min(ceil_div(rows, a->tile_rows), most / std::max<int64_t>(1, pairs));
     int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
     if (q->window > 0)
         tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
     const int64_t blocks = std::max<int64_t>(1, pairs * tiles), fill = a->tile_rows <= 32 ? 1024 : 512;
     int64_t splits = std::max(std::min(ceil_div(tokens, 256), fill / blocks), a->tile_rows <= 32 ? ceil_div(tokens, 4096) : 1);
-    splits = std::min(std::max<int64_t>(1, splits), INT32_MAX / 4 / blocks);
+    if (ceil_div((int64_t)b->total * q->q_heads, join_rows(c->head_dim)) > kMostThreads / kJoinThreads)
+        splits = 1;
+    splits = std::min(std::max<int64_t>(1, splits), most / blocks);
     const int64_t groups = ceil_div(std::max<int64_t>(1, tokens), 16);
     a->per = (int32_t)(ceil_div(ceil_div(groups, splits), 8) * 8);
     a->tiles = (int32_t)tiles;
     a->splits = (int32_t)ceil_div(groups, a->per);
+    return SPLITZIP_OK;
+}
+
+// Launch of a weigh call.
+int plan_weigh(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, AttendArgs *a)
+{
+    const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
+    KV4_REQUIRE(pairs <= 1 << 22, "more than 2^22 sequences and heads");
+    const int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
+    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
+    // Up to 16 rows stay in registers: 64 decode steps of 8 rows 52 us, by rows_kernel 135.
+    a->tile_rows = rows <= kStepRows ? kStepRows : 0;
+    if (a->tile_rows == kStepRows) {
+        // 256 tokens a workgroup at least (one turn of each wave), and 2048 workgroups at most (the same at
+        // 4096; 1024 took 63 us for 57)
+        a->splits = (int32_t)std::min<int64_t>(std::max<int64_t>(1, 2048 / pairs), tokens / 256 + 1);
+    } else {
+        // a launch that would be too large has fewer, which take tokens in turn
+        a->splits = (int32_t)std::min(tokens / weigh_tokens(c->head_dim) + 1, kMostThreads / kWeighThreads / pairs);
+    }
     return SPLITZIP_OK;
 }
 
@@ -252,8 +275,7 @@ int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
     Device d(cache->device);
     if (d.status)
         return d.status;
-    launch_attend(a, cache->head_dim, queries->dtype, static_cast<hipStream_t>(stream));
-    return Device::launched();
+    return Device::launched(launch_attend(a, cache->head_dim, queries->dtype, static_cast<hipStream_t>(stream)));
 }
 
 int splitzip_kv4_weigh(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
@@ -269,15 +291,13 @@ int splitzip_kv4_weigh(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
     if (a.b.total == 0)
         return SPLITZIP_OK;
     KV4_REQUIRE(lse, "lse is null");
-    KV4_REQUIRE((int64_t)a.b.n_seqs * a.c.heads <= 1 << 22, "more than 2^22 sequences and heads");
+    if (int e = plan_weigh(cache, batch, &a))
+        return e;
     a.lse_in = lse;
-    const int64_t cap = (int64_t)a.b.table_width << a.c.page_shift;
-    const int max_len = (int)std::min<int64_t>(batch->max_len, cap);
-    const int max_q = (int)std::max<int64_t>(1, std::min<int64_t>(batch->max_q, batch->total));
     Device d(cache->device);
     if (d.status)
         return d.status;
-    launch_weigh(a, cache->head_dim, queries->dtype, max_q, max_len, static_cast<hipStream_t>(stream));
+    launch_weigh(a, cache->head_dim, queries->dtype, static_cast<hipStream_t>(stream));
     return Device::launched();
 }
 
@@ -321,23 +341,50 @@ int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
 int splitzip_kv4_launches(int32_t op, const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
                           const splitzip_kv4_queries *queries, int32_t budget, uint64_t workgroups[2], uint32_t threads[2])
 {
-    KV4_REQUIRE(op == SPLITZIP_KV4_EVICT, "no such operator");
     KV4_REQUIRE(workgroups && threads, "workgroups or threads is null");
     for (int i = 0; i < 2; ++i)
         workgroups[i] = threads[i] = 0;
-    EvictArgs a;
+    if (op == SPLITZIP_KV4_EVICT) {
+        EvictArgs a;
+        if (int e = check_cache(cache, &a.c))
+            return e;
+        if (int e = check_batch(batch, a.c, false, &a.b))
+            return e;
+        if (a.b.n_seqs == 0)
+            return SPLITZIP_OK;
+        if (int e = plan_evict(batch, budget, &a))
+            return e;
+        workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads;
+        threads[0] = kChooseThreads;
+        workgroups[1] = workgroups[0] * a.turns;
+        threads[1] = kMoveThreads;
+        return SPLITZIP_OK;
+    }
+    KV4_REQUIRE(op == SPLITZIP_KV4_ATTEND || op == SPLITZIP_KV4_WEIGH, "no such operator");
+    AttendArgs a;
     if (int e = check_cache(cache, &a.c))
         return e;
-    if (int e = check_batch(batch, a.c, false, &a.b))
+    if (int e = check_batch(batch, a.c, true, &a.b))
         return e;
-    if (a.b.n_seqs == 0)
+    if (int e = check_queries(queries, batch, cache, &a))
+        return e;
+    if (a.b.total == 0)
         return SPLITZIP_OK;
-    if (int e = plan_evict(batch, budget, &a))
+    if (op == SPLITZIP_KV4_WEIGH) {
+        if (int e = plan_weigh(cache, batch, &a))
+            return e;
+        workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads * a.splits;
+        threads[0] = kWeighThreads;
+        return SPLITZIP_OK;
+    }
+    if (int e = plan(cache, batch, queries, &a))
         return e;
-    workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads;
-    threads[0] = kChooseThreads;
-    workgroups[1] = workgroups[0] * a.turns;
-    threads[1] = kMoveThreads;
+    workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads * a.tiles * a.splits;
+    threads[0] = attend_threads(cache->head_dim, a.tile_rows);
+    if (a.splits > 1) {
+        workgroups[1] = ceil_div(a.b.total * a.q_heads, join_rows(cache->head_dim));
+        threads[1] = kJoinThreads;
+    }
     return SPLITZIP_OK;
 }
 

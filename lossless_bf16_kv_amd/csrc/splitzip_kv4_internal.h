@@ -54,7 +54,7 @@ struct AttendArgs {
     const float *lse_in;     // weigh
     float *part_o, *part_ml; // partial results of splits > 1: [split][row][D], [split][row][2]
     int32_t splits, tiles;   // workgroups along the tokens and along the rows of a sequence and head
-    int32_t per, tile_rows;  // attend: groups of 16 tokens a split, rows a tile
+    int32_t per, tile_rows;  // attend: groups of 16 tokens a split, rows a tile; weigh: rows a tile, 0: no tiles
 };
 
 struct EvictArgs {
@@ -75,8 +75,12 @@ constexpr int kChooseThreads = 1024, kMoveThreads = 256, kMoveTokens = 128;
 void launch_append(const AppendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_read(const ReadArgs &a, int head_dim, int dtype, hipStream_t s);
 int attend_rows(int head_dim, int64_t rows);   // rows of a workgroup for this many rows a sequence
-void launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
-void launch_weigh(const AttendArgs &a, int head_dim, int dtype, int max_q, int max_len, hipStream_t s);
+int attend_threads(int head_dim, int tile_rows);
+int join_rows(int head_dim);                   // rows of a workgroup of join_kernel
+constexpr int kJoinThreads = 256, kWeighThreads = 256, kStepRows = 16;
+constexpr int weigh_tokens(int head_dim) { return head_dim == 256 ? 128 : 256; }     // of a workgroup of rows_kernel
+hipError_t launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
+void launch_weigh(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
 hipError_t launch_evict(const EvictArgs &a, int head_dim, hipStream_t s);
 
 // ---- device ---------------------------------------------------------------------------------

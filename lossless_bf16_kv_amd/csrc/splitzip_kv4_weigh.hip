@@ -20,13 +20,11 @@
 // see nothing left out took it there from 572 us.
 #include "splitzip_kv4_tiles.h"
 
-#include <algorithm>
-
 namespace sz {
 namespace kv4 {
 namespace {
 
-constexpr int kLanes = 256;
+constexpr int kLanes = kWeighThreads;
 // Query and head of a row, moved on without a division.
 struct RowAt {
     int query, head;
@@ -42,7 +40,7 @@ struct RowAt {
 };
 
 template <int D>
-constexpr int kWeighTokens = D == 256 ? 128 : 256;      // of a workgroup of rows_kernel
+constexpr int kWeighTokens = weigh_tokens(D);
 
 // One turn of a wave in LDS, 64 tokens: K's codes of four groups (8 D bytes each: D >= 128 16 bytes a
 // lane in lane order, D = 256 two of them; D = 64 as in the cache), their scales (D = 64 as in the
@@ -496,35 +494,26 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
 }
 
 template <int D, int T>
-void weigh_dt(AttendArgs a, int max_q, int max_len, hipStream_t s)
+void weigh_dt(const AttendArgs &a, hipStream_t s)
 {
-    const int64_t pairs = (int64_t)a.b.n_seqs * a.c.heads;
-    if ((int64_t)max_q * a.group <= 16) {
-        // Up to 16 rows stay in registers: 64 decode steps of 8 rows 52 us, by rows_kernel 135.
-        // 256 tokens a workgroup at least (one turn of each wave), and 2048 workgroups at most (the same at
-        // 4096; 1024 took 63 us for 57)
-        const int64_t most = std::max<int64_t>(1, 2048 / pairs);
-        a.splits = (int32_t)std::min<int64_t>(most, max_len / 256 + 1);
-        step_kernel<D, T><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
-    } else {
-        a.splits = max_len / kWeighTokens<D> + 1;
-        if (pairs * a.splits > INT32_MAX / 2)
-            a.splits = 1;
-        rows_kernel<D, T><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
-    }
+    const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.splits);
+    if (a.tile_rows == kStepRows)
+        step_kernel<D, T><<<grid, kLanes, 0, s>>>(a);
+    else
+        rows_kernel<D, T><<<grid, kLanes, 0, s>>>(a);
 }
 
 }  // namespace
 
-void launch_weigh(const AttendArgs &a, int head_dim, int dtype, int max_q, int max_len, hipStream_t s)
+void launch_weigh(const AttendArgs &a, int head_dim, int dtype, hipStream_t s)
 {
     const bool b = dtype == SPLITZIP_KV4_BF16;
     if (head_dim == 64)
-        b ? weigh_dt<64, SPLITZIP_KV4_BF16>(a, max_q, max_len, s) : weigh_dt<64, SPLITZIP_KV4_FP16>(a, max_q, max_len, s);
+        b ? weigh_dt<64, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<64, SPLITZIP_KV4_FP16>(a, s);
     else if (head_dim == 128)
-        b ? weigh_dt<128, SPLITZIP_KV4_BF16>(a, max_q, max_len, s) : weigh_dt<128, SPLITZIP_KV4_FP16>(a, max_q, max_len, s);
+        b ? weigh_dt<128, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<128, SPLITZIP_KV4_FP16>(a, s);
     else
-        b ? weigh_dt<256, SPLITZIP_KV4_BF16>(a, max_q, max_len, s) : weigh_dt<256, SPLITZIP_KV4_FP16>(a, max_q, max_len, s);
+        b ? weigh_dt<256, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<256, SPLITZIP_KV4_FP16>(a, s);
 }
 
 }  // namespace kv4

@@ -74,3 +74,27 @@ def test_evict_launch_goes_by_the_longest_sequence(max_len, turns):
 def test_evict_launch_goes_by_the_table():
     _, move = launches(EVICT, b=batch(max_len=MOST), budget=1 << 20)          # 5 pages of 64 tokens
     assert move == (24 * 3, 256)
+
+
+ATTEND, WEIGH = 0, 1
+
+
+# seqs, rows a sequence, KV heads, group, D, tokens a table holds; max_q: all rows, as a caller without a better guess says
+@pytest.mark.parametrize("op", [ATTEND, WEIGH])
+@pytest.mark.parametrize("seqs,n,heads,group,d,tokens", [
+    (1024, 32, 8, 8, 128, 8192), (512, 128, 8, 8, 128, 8192), (256, 64, 8, 8, 256, 1 << 20), (512, 100, 8, 8, 128, 1 << 20),
+    (1 << 18, 1, 8, 8, 128, 1 << 20), (1 << 18, 3, 16, 4, 64, 1 << 20), (1, 1 << 20, 1, 64, 128, 1 << 20), (1, 1, 1, 1, 64, 16),
+    (4, 1 << 22, 1, 16, 256, 1 << 24)])
+def test_attend_and_weigh_launches(op, seqs, n, heads, group, d, tokens):
+    width = tokens // 16
+    b = batch(n_seqs=seqs, total=seqs * n, cu_seqlens=1 << 20, table_width=width, table_stride=width, max_q=seqs * n, max_len=tokens)
+    got = launches(op, c=cache(page_size=16, kv_heads=heads, head_dim=d), b=b,
+                   q=queries(q_heads=heads * group, token_stride=heads * group * d, head_stride=d))
+    assert got and got[0][0] % (seqs * heads) == 0
+    assert all(g * t < 1 << 32 for g, t in got), got
+
+
+@pytest.mark.parametrize("op", ["attend", "weigh"])
+@pytest.mark.parametrize("seqs", [1 << 22, 1 << 24])
+def test_attend_and_weigh_of_too_many_heads(op, seqs):
+    refused(op, "sequences and heads", b=batch(n_seqs=seqs, total=seqs, max_q=1))
