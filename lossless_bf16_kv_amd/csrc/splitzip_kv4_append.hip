@@ -22,7 +22,7 @@ namespace sz {
 namespace kv4 {
 namespace {
 
-constexpr int kLanes = 256;
+constexpr int kLanes = kRowThreads;
 
 __device__ __forceinline__ void load8(const void *p, int64_t at, int dtype, bool wide, float (&x)[8])
 {

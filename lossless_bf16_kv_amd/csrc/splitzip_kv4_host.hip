@@ -86,6 +86,12 @@ int check_batch(const splitzip_kv4_batch *b, const Cache &c, bool rows, Batch *o
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Threads of an append or read launch: a lane takes 8 channels, a workgroup whole rows of one head.
+int64_t row_launch(const Batch &b, const Cache &c, int head_dim)
+{
+    return ceil_div(b.total, kRowThreads / (head_dim / 8)) * c.heads * kRowThreads;
+}
+
 int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, const splitzip_kv4_cache *c, AttendArgs *a)
 {
     KV4_REQUIRE(q, "queries is null");
@@ -193,7 +199,7 @@ int splitzip_kv4_append(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
     const int size = dtype == SPLITZIP_KV4_FP32 ? 4 : 2;
     KV4_REQUIRE(reinterpret_cast<uintptr_t>(k) % size == 0 && reinterpret_cast<uintptr_t>(v) % size == 0,
                 "k or v is not aligned to its type");
-    KV4_REQUIRE(a.b.total * a.c.heads < INT32_MAX, "total * kv_heads must be below 2^31");
+    KV4_REQUIRE(row_launch(a.b, a.c, cache->head_dim) <= kMostThreads, "more rows and heads than a launch holds");
     const int unit = 16 / size;
     a.k = k;
     a.v = v;
@@ -222,7 +228,7 @@ int splitzip_kv4_read(const splitzip_kv4_cache *cache, const splitzip_kv4_batch 
     if (a.b.total == 0)
         return SPLITZIP_OK;
     KV4_REQUIRE(k && v && aligned16(k) && aligned16(v), "k or v is null or not 16-byte aligned");
-    KV4_REQUIRE(a.b.total * a.c.heads < INT32_MAX, "total * kv_heads must be below 2^31");
+    KV4_REQUIRE(row_launch(a.b, a.c, cache->head_dim) <= kMostThreads, "more rows and heads than a launch holds");
     a.k = k;
     a.v = v;
     Device d(cache->device);

@@ -70,7 +70,7 @@ struct EvictArgs {
 
 // HIP launches fewer than 2^32 threads at a time.
 constexpr int64_t kMostThreads = UINT32_MAX;
-constexpr int kChooseThreads = 1024, kMoveThreads = 256, kMoveTokens = 128;
+constexpr int kRowThreads = 256, kChooseThreads = 1024, kMoveThreads = 256, kMoveTokens = 128;
 
 void launch_append(const AppendArgs &a, int head_dim, int dtype, hipStream_t s);
 void launch_read(const ReadArgs &a, int head_dim, int dtype, hipStream_t s);

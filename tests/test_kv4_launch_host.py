@@ -98,3 +98,10 @@ def test_attend_and_weigh_launches(op, seqs, n, heads, group, d, tokens):
 @pytest.mark.parametrize("seqs", [1 << 22, 1 << 24])
 def test_attend_and_weigh_of_too_many_heads(op, seqs):
     refused(op, "sequences and heads", b=batch(n_seqs=seqs, total=seqs, max_q=1))
+
+
+@pytest.mark.parametrize("op", ["append", "read"])
+@pytest.mark.parametrize("d,rows,heads", [(64, 1 << 26, 8), (128, 1 << 25, 8), (256, 1 << 24, 8), (256, (1 << 27) + 1, 1)])
+def test_append_and_read_of_too_many_rows(op, d, rows, heads):
+    b = batch(n_seqs=1, total=rows, cu_seqlens=1 << 20)
+    refused(op, "more rows and heads than a launch holds", c=cache(head_dim=d, kv_heads=heads), b=b)
