@@ -97,7 +97,8 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
     KV4_REQUIRE(q, "queries is null");
     KV4_REQUIRE(q->dtype == SPLITZIP_KV4_BF16 || q->dtype == SPLITZIP_KV4_FP16, "queries must be bf16 or fp16");
     KV4_REQUIRE(q->q_heads >= c->kv_heads && q->q_heads % c->kv_heads == 0, "q_heads must be a multiple of kv_heads");
-    KV4_REQUIRE(b->total * q->q_heads < INT32_MAX, "total * q_heads must be below 2^31");
+    // kernels count up to 256 rows past a sequence's last in 32 bits
+    KV4_REQUIRE(b->total * q->q_heads <= INT32_MAX - 65536, "total * q_heads must be below 2^31 - 65536");
     KV4_REQUIRE(q->window >= 0 && q->sinks >= 0, "window or sinks is negative");
     KV4_REQUIRE(std::isfinite(q->scale), "scale is not finite");
     KV4_REQUIRE(q->q || b->total == 0, "q is null");

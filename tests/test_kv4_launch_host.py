@@ -105,3 +105,11 @@ def test_attend_and_weigh_of_too_many_heads(op, seqs):
 def test_append_and_read_of_too_many_rows(op, d, rows, heads):
     b = batch(n_seqs=1, total=rows, cu_seqlens=1 << 20)
     refused(op, "more rows and heads than a launch holds", c=cache(head_dim=d, kv_heads=heads), b=b)
+
+
+# The kernels count up to 256 rows past a sequence's last in 32 bits.
+@pytest.mark.parametrize("op", ["attend", "weigh"])
+@pytest.mark.parametrize("total,heads", [(MOST - 1, 1), (MOST - 255, 1), (MOST - 65535, 1), ((1 << 30) - 1, 2), ((1 << 25) - 1, 64)])
+def test_rows_of_nearly_2_31(op, total, heads):
+    b = batch(n_seqs=1, total=total, cu_seqlens=1 << 20)
+    refused(op, "total * q_heads must be below 2^31 - 65536", c=cache(kv_heads=1), b=b, q=queries(q_heads=heads))
