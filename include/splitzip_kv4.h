@@ -71,8 +71,8 @@ typedef struct splitzip_kv4_cache {
  * them; its n = cu_seqlens[s + 1] - cu_seqlens[s] new tokens or queries are rows
  * cu_seqlens[s] .. of the call's tensors and stand at its last n tokens (cu_seqlens NULL: one
  * row a sequence).  total: rows of those tensors.  max_q and max_len say how many queries and
- * tokens a sequence is expected to have; they choose the launch, and the results hold whatever
- * they say.
+ * tokens a sequence is expected to have; they choose the launch and with it attend's workspace,
+ * and the results hold whatever they say.
  */
 typedef struct splitzip_kv4_batch {
     const int32_t *table;
@@ -118,7 +118,7 @@ int splitzip_kv4_append(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
 int splitzip_kv4_read(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch, void *k, void *v,
                       int32_t dtype, void *stream);
 
-/* Bytes of the workspace that splitzip_kv4_attend wants for this call (0: none). */
+/* Bytes of the workspace that splitzip_kv4_attend wants for this call (0: none; at most 512 MiB). */
 int splitzip_kv4_attend_workspace(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
                                   const splitzip_kv4_queries *queries, uint64_t *bytes);
 

@@ -115,10 +115,17 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
     return SPLITZIP_OK;
 }
 
+// Bytes of a split's partial results.
+int64_t split_bytes(const AttendArgs &a, int head_dim) { return a.b.total * a.q_heads * (head_dim + 2) * 4; }
+
 // Launch of an attend call: rows of a workgroup, row tiles, splits along the tokens.  The lengths are
 // known only to the GPU.  A split takes 4096 tokens, so that a few long sequences among short ones do
 // not outlast the others (256 decode steps of 128 .. 8192 tokens: 251 us, unsplit 263, at 2048 264);
-// fewer, but 256 at least, where there would be fewer workgroups than the GPU holds at a time.
+// fewer, but 256 at least, where there would be fewer workgroups than the GPU holds at a time; and more
+// where there would be over 16 times as many, since a length that nobody has costs a workgroup that ends at
+// once and a place in the workspace (256 steps of up to 1024 tokens on tables of 2^20: 64 us and 70 MiB
+// for 1030 us and 2084 MiB).  Two steps of 2^19 tokens among 252 short ones, where that leaves parts of
+// 2^17, took 1221 us for 1176.
 int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzip_kv4_queries *q, AttendArgs *a)
 {
     const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
@@ -132,7 +139,10 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
     if (q->window > 0)
         tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
     const int64_t blocks = std::max<int64_t>(1, pairs * tiles), fill = a->tile_rows <= 32 ? 1024 : 512;
-    int64_t splits = std::max(std::min(ceil_div(tokens, 256), fill / blocks), a->tile_rows <= 32 ? ceil_div(tokens, 4096) : 1);
+    const int64_t even = a->tile_rows <= 32 ? std::min(ceil_div(tokens, 4096), 16 * fill / blocks) : 1;
+    int64_t splits = std::max(std::min(ceil_div(tokens, 256), fill / blocks), even);
+    // hints that say too little do not make it larger
+    splits = std::min<int64_t>(splits, (512ll << 20) / std::max<int64_t>(1, split_bytes(*a, c->head_dim)));
     if (ceil_div((int64_t)b->total * q->q_heads, join_rows(c->head_dim)) > kMostThreads / kJoinThreads)
         splits = 1;
     splits = std::min(std::max<int64_t>(1, splits), most / blocks);
@@ -163,10 +173,7 @@ int plan_weigh(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, AttendA
     return SPLITZIP_OK;
 }
 
-uint64_t workspace_of(const AttendArgs &a, int head_dim)
-{
-    return a.splits == 1 ? 0 : (uint64_t)a.splits * a.b.total * a.q_heads * (head_dim + 2) * 4;
-}
+uint64_t workspace_of(const AttendArgs &a, int head_dim) { return a.splits == 1 ? 0 : a.splits * split_bytes(a, head_dim); }
 
 // Launches of an evict call: a workgroup of move_kernel for every 128 tokens that a sequence and head may
 // keep.  A launch that would be too large has fewer, which take tokens in turn.

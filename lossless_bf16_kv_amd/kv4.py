@@ -238,7 +238,7 @@ class KV4Cache:
         lse fp32 [rows, q_heads].  Query i of a sequence stands at token p = len - n + i and sees
         tokens j <= p with j > p - window (None: all) or j < sinks.  A query that sees nothing gets
         out = 0, lse = -inf.  ``scale``: default head_dim ** -0.5.  ``max_q`` and ``max_len`` (most
-        queries and tokens of a sequence, from the host) only choose the launch."""
+        queries and tokens of a sequence, from the host) only choose the launch and its workspace."""
         qs = self._queries(q, scale, window, sinks)
         rows, heads, _ = q.shape
         b = self._batch(table, lens, cu, rows, max_q, max_len)

@@ -113,3 +113,35 @@ def test_append_and_read_of_too_many_rows(op, d, rows, heads):
 def test_rows_of_nearly_2_31(op, total, heads):
     b = batch(n_seqs=1, total=total, cu_seqlens=1 << 20)
     refused(op, "total * q_heads must be below 2^31 - 65536", c=cache(kv_heads=1), b=b, q=queries(q_heads=heads))
+
+
+def workspace(seqs, n, tokens, heads=8, group=8, d=128, max_q=None, max_len=None):
+    width, need = tokens // 16, ctypes.c_uint64()
+    c = cache(page_size=16, kv_heads=heads, head_dim=d)
+    b = batch(n_seqs=seqs, total=seqs * n, cu_seqlens=1 << 20, table_width=width, table_stride=width, max_q=max_q or n,
+              max_len=max_len or tokens)
+    q = queries(q_heads=heads * group, token_stride=heads * group * d, head_stride=d)
+    refs = [ctypes.byref(x) for x in (c, b, q, need)]
+    assert kv4._lib().splitzip_kv4_attend_workspace(*refs) == sz.OK
+    got = launches(ATTEND, c, b, q)
+    return need.value, got[0][0]
+
+
+# Splits that are there for balance are few where there are many sequences, however long the table could make these.
+@pytest.mark.parametrize("seqs,n,tokens,most", [(256, 1, 1 << 20, 80 << 20), (256, 1, 1 << 17, 80 << 20), (1024, 4, 1 << 17, 300 << 20),
+                                                (4096, 1, 1 << 20, 0), (1, 1, 1 << 20, 80 << 20), (32, 1, 1 << 20, 80 << 20)])
+def test_attend_workspace_of_wide_tables(seqs, n, tokens, most):
+    got, groups = workspace(seqs, n, tokens)
+    assert got <= most and groups <= max(seqs * 8, 16 * 1024)
+
+
+def test_attend_workspace_has_an_end():
+    # hints that say far too little: one query a sequence where there are thousands
+    got, _ = workspace(1, 4096, 1 << 17, max_q=1)
+    assert 0 < got <= 512 << 20
+
+
+@pytest.mark.parametrize("seqs,n,tokens,splits", [(256, 1, 8192, 2), (32, 1, 32768, 8), (1, 1, 4096, 16), (64, 1, 1 << 17, 32)])
+def test_attend_splits(seqs, n, tokens, splits):
+    got, groups = workspace(seqs, n, tokens)
+    assert groups == seqs * 8 * splits and got == splits * seqs * n * 64 * (128 + 2) * 4
