@@ -72,7 +72,7 @@ typedef struct splitzip_kv4_cache {
  * cu_seqlens[s] .. of the call's tensors and stand at its last n tokens (cu_seqlens NULL: one
  * row a sequence).  total: rows of those tensors.  max_q and max_len say how many queries and
  * tokens a sequence is expected to have; they choose the launch and with it attend's workspace,
- * and the results hold whatever they say.
+ * and the results hold whatever they say.  max_q 0: not known.
  */
 typedef struct splitzip_kv4_batch {
     const int32_t *table;

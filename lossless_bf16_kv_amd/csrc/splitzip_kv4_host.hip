@@ -118,6 +118,13 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
 // Bytes of a split's partial results.
 int64_t split_bytes(const AttendArgs &a, int head_dim) { return a.b.total * a.q_heads * (head_dim + 2) * 4; }
 
+// Rows of a sequence and KV head that a launch is made for: the most there are, or the mean where nobody says.
+int64_t expected_rows(const splitzip_kv4_batch &b, int group)
+{
+    const int64_t q = b.max_q > 0 ? std::min<int64_t>(b.max_q, b.total) : ceil_div(b.total, std::max(1, b.n_seqs));
+    return std::max<int64_t>(1, q) * group;
+}
+
 // Launch of an attend call: rows of a workgroup, row tiles, splits along the tokens.  The lengths are
 // known only to the GPU.  A split takes 4096 tokens, so that a few long sequences among short ones do
 // not outlast the others (256 decode steps of 128 .. 8192 tokens: 251 us, unsplit 263, at 2048 264);
@@ -128,24 +135,33 @@ int64_t split_bytes(const AttendArgs &a, int head_dim) { return a.b.total * a.q_
 // 2^17, took 1221 us for 1176.
 int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzip_kv4_queries *q, AttendArgs *a)
 {
-    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
+    const int64_t rows = expected_rows(*b, a->group);
     a->tile_rows = attend_rows(c->head_dim, rows);
     const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
     // workgroups that a launch holds; fewer tiles and splits than there could be take rows and tokens in turn
     const int64_t most = kMostThreads / attend_threads(c->head_dim, a->tile_rows);
     KV4_REQUIRE(pairs <= most, "too many sequences and heads");
-    const int64_t tiles = std::min(ceil_div(rows, a->tile_rows), most / std::max<int64_t>(1, pairs));
+    // Without max_q a sequence may have more rows than expected, all of them at most: twice the tiles, up to 4096
+    // workgroups, and rows in turn beyond.  An odd number of tiles, since the ones with rows would meet on
+    // few CUs where it is a multiple of their number.  Against all rows as every sequence's (us): 64 requests
+    // of 3 drafts 83 for 489, 256 single tokens 238 for 4161, 16 prompts of 64 .. 4096 tokens 1044 for
+    // 1211, a prompt of 2048 among 63 single tokens 620 for 642; up to 16384 workgroups 107, 242, 1060, 645.
+    const int64_t expected = ceil_div(rows, a->tile_rows);
+    int64_t tiles = expected;
+    if (b->max_q == 0)
+        tiles = std::min(std::max(2 * expected, 4096 / std::max<int64_t>(1, pairs)), ceil_div(b->total * a->group, a->tile_rows)) | 1;
+    tiles = std::min(tiles, most / std::max<int64_t>(1, pairs));
     int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
     if (q->window > 0)
         tokens = std::min<int64_t>(tokens, (int64_t)q->window + q->sinks + 32 + rows / a->group);
-    const int64_t blocks = std::max<int64_t>(1, pairs * tiles), fill = a->tile_rows <= 32 ? 1024 : 512;
+    const int64_t blocks = std::max<int64_t>(1, pairs * expected), fill = a->tile_rows <= 32 ? 1024 : 512;
     const int64_t even = a->tile_rows <= 32 ? std::min(ceil_div(tokens, 4096), 16 * fill / blocks) : 1;
     int64_t splits = std::max(std::min(ceil_div(tokens, 256), fill / blocks), even);
     // hints that say too little do not make it larger
     splits = std::min<int64_t>(splits, (512ll << 20) / std::max<int64_t>(1, split_bytes(*a, c->head_dim)));
     if (ceil_div((int64_t)b->total * q->q_heads, join_rows(c->head_dim)) > kMostThreads / kJoinThreads)
         splits = 1;
-    splits = std::min(std::max<int64_t>(1, splits), most / blocks);
+    splits = std::min(std::max<int64_t>(1, splits), most / std::max<int64_t>(1, pairs * tiles));
     const int64_t groups = ceil_div(std::max<int64_t>(1, tokens), 16);
     a->per = (int32_t)(ceil_div(ceil_div(groups, splits), 8) * 8);
     a->tiles = (int32_t)tiles;
@@ -159,7 +175,7 @@ int plan_weigh(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, AttendA
     const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
     KV4_REQUIRE(pairs <= 1 << 22, "more than 2^22 sequences and heads");
     const int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
-    const int64_t rows = std::max<int64_t>(1, std::min<int64_t>(b->max_q, b->total)) * a->group;
+    const int64_t rows = expected_rows(*b, a->group);
     // Up to 16 rows stay in registers: 64 decode steps of 8 rows 52 us, by rows_kernel 135.
     a->tile_rows = rows <= kStepRows ? kStepRows : 0;
     if (a->tile_rows == kStepRows) {

@@ -1,6 +1,6 @@
 """GPU tests of the 4-bit KV cache at the ends of its range, against the 64-bit implementations of
 tests/kv4_reference.py: the largest values that the format holds,
-hints that say too little."""
+hints that say too little, too much or nothing."""
 from __future__ import annotations
 
 import math
@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import kv4_reference as ref
-from test_gpu_kv4 import BF16, Setup, check_evict
+from test_gpu_kv4 import BF16, FP16, Setup, check_attend, check_evict
 
 pytestmark = pytest.mark.gpu
 
@@ -33,7 +33,7 @@ def test_attend_largest_values(d, count):
     q = torch.zeros(s.total, 4, d, dtype=BF16)
     q[:, :, 0] = 1.0
     scale = math.log(2)
-    out, lse = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, scale=scale)
+    out, lse = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, max_q=count, scale=scale)
     eo, to, el, tl = ref.attend(ref.Cache(s.cache), q.double(), s.rows(), s.lens_l, s.counts, scale, None, 0, BF16)
     assert out.isfinite().all()
     assert ((out.cpu().double() - eo).abs() <= to).all()
@@ -46,3 +46,38 @@ def test_evict_hint_that_says_too_little(d, max_len):
     # a move workgroup takes several turns, the last of them short
     s = Setup([0, 1, 700, 523, 900], [1] * 5, heads=2, d=d, page=32, extra=100, seed=d)
     check_evict(s, lambda q, n: torch.rand(2, n, generator=s.g), 523, 4, 100, max_len=max_len)
+
+
+# queries of the longest sequence: with a group of 4, 4, 20, 52, 100 and 300 rows
+COUNTS = [(1, 1, 1, 0), (5, 2, 1, 0), (13, 1, 5, 0), (25, 12, 5, 2), (75, 30, 3, 0)]
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("dtype", [BF16, FP16])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_attend_row_tiles_by_hint(d, dtype, counts):
+    # a tile is as long as the longest sequence's rows, or as the mean's where nobody says
+    s = Setup([401, 130, 5, 17], counts, heads=2, d=d, page=32, seed=d + counts[0])
+    for kw in ({"max_q": counts[0]}, {"max_q": 10 ** 6}, {}):
+        check_attend(s, 8, dtype, window=50, sinks=7, **kw)
+        check_attend(s, 8, dtype, **kw)
+    s.cache.check()
+
+
+@pytest.mark.parametrize("counts", COUNTS)
+@pytest.mark.parametrize("d,dtype", [(64, FP16), (128, BF16), (256, FP16)])
+def test_attend_nan_in_row_tiles_by_hint(d, dtype, counts):
+    s = Setup([401, 130, 5, 17], counts, heads=2, d=d, page=32, seed=counts[0])
+    for q, j, h in ((0, 398, 0), (0, 20, 1), (1, 129, 1), (1, 3, 0), (2, 0, 1), (0, 352, 1)):
+        s.cache.v_scales[int(s.table_h[q, j // 32]), h, j % (d // 32), j % 32] = 255
+    for q, j in ((0, 380), (1, 127)):
+        s.cache.k_scales[int(s.table_h[q, j // 32]), 1, j % 32, 0] = 255
+    for window, sinks in ((None, 0), (40, 2)):
+        check_attend(s, 4, dtype, window=window, sinks=sinks, max_q=counts[0])
+
+
+def test_attend_one_long_sequence_among_many():
+    # rows past the launch's tiles are taken in turn: 63 single queries and one sequence of 500
+    s = Setup([40] * 63 + [500], [1] * 63 + [500], heads=8, d=64, page=64)
+    check_attend(s, 8, BF16)
+    check_attend(s, 32, BF16, window=30, sinks=3)

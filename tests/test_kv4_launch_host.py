@@ -3,8 +3,10 @@ here reaches the GPU."""
 from __future__ import annotations
 
 import ctypes
+import types
 
 import pytest
+import torch
 
 import lossless_bf16_kv_amd as sz
 from lossless_bf16_kv_amd import kv4
@@ -145,3 +147,32 @@ def test_attend_workspace_has_an_end():
 def test_attend_splits(seqs, n, tokens, splits):
     got, groups = workspace(seqs, n, tokens)
     assert groups == seqs * 8 * splits and got == splits * seqs * n * 64 * (128 + 2) * 4
+
+
+# max_q 0: not known.  The rows of a tile go by the mean, and empty workgroups have an end.
+@pytest.mark.parametrize("seqs,n,group,threads,least", [(64, 3, 4, 256, 1), (256, 1, 8, 256, 1), (64, 100, 4, 512, 2), (16, 2048, 4, 512, 32),
+                                                        (1, 4096, 4, 512, 64), (1, 1, 8, 256, 1)])
+def test_attend_launch_without_max_q(seqs, n, group, threads, least):
+    b = batch(n_seqs=seqs, total=seqs * n, cu_seqlens=1 << 20, table_width=64, table_stride=64, max_q=0, max_len=256)     # no splits
+    (groups, got), *_ = launches(ATTEND, b=b, q=queries(q_heads=8 * group, token_stride=1024 * group))
+    tiles = groups // (seqs * 8)
+    assert got == threads and tiles >= least
+    if seqs > 1:
+        assert groups <= max(4096 + seqs * 8, 3 * least * seqs * 8)
+
+
+def test_weigh_launch_without_max_q():
+    # up to 16 rows a sequence stay in registers
+    b = batch(n_seqs=64, total=192, cu_seqlens=1 << 20, table_width=64, table_stride=64, max_len=4096)
+    got = []
+    for max_q in (0, 3, 192):
+        b.max_q = max_q
+        got.append(launches(WEIGH, b=b, q=queries(q_heads=32, token_stride=4096)))
+    assert got[0] == got[1] != got[2]
+
+
+def test_python_says_that_it_does_not_know():
+    t = torch.zeros(3, 4, dtype=torch.int32)
+    me = types.SimpleNamespace(page_size=16, _int32=lambda t, name, shape=None: 0)
+    assert kv4.KV4Cache._batch(me, t, t, t, 300, None, None).max_q == 0
+    assert kv4.KV4Cache._batch(me, t, t, t, 300, 7, None).max_q == 7
