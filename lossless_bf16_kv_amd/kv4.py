@@ -169,7 +169,7 @@ class KV4Cache:
                                table.stride(0), total, width, n, 1, max_len if max_len < _BIG else _BIG)
         if cu is not None:
             b.cu_seqlens = self._int32(cu, "cu", (n + 1,))
-            b.max_q = 0 if max_q is None else max_q
+            b.max_q = 0 if max_q is None else max_q if max_q < _BIG else _BIG
         elif total != n:
             raise ValueError(f"without cu there is one row a sequence: {total} rows, {n} sequences")
         return b

@@ -176,3 +176,11 @@ def test_python_says_that_it_does_not_know():
     me = types.SimpleNamespace(page_size=16, _int32=lambda t, name, shape=None: 0)
     assert kv4.KV4Cache._batch(me, t, t, t, 300, None, None).max_q == 0
     assert kv4.KV4Cache._batch(me, t, t, t, 300, 7, None).max_q == 7
+
+
+@pytest.mark.parametrize("max_q", [MOST, MOST + 1, 1 << 32, (1 << 32) + 1])
+def test_python_hint_past_32_bits_is_not_cut(max_q):
+    t = torch.zeros(3, 4, dtype=torch.int32)
+    me = types.SimpleNamespace(page_size=16, _int32=lambda t, name, shape=None: 0)
+    assert kv4.KV4Cache._batch(me, t, t, t, 300, max_q, None).max_q == MOST
+    assert kv4.KV4Cache._batch(me, t, t, t, 300, None, max_q).max_len == MOST
