@@ -284,11 +284,13 @@ class KV4Cache:
         return out_lens, kept
 
     def check(self) -> None:
-        """Waits for the GPU and raises if a call since the last check met a page number, a length or
-        row offsets out of range."""
+        """Waits for the GPU, all its streams, and raises if a call since the last check met a page number, a
+        length or row offsets out of range."""
+        import torch
+        torch.cuda.synchronize(self.device)
         bits = int(self.status.item())
         if bits:
-            self.status.zero_()
+            self.status.bitwise_and_(~bits)                     # a bit set meanwhile stays for the next check
             what = [t for b, t in ((BAD_PAGE, "a page number outside the cache"),
                                    (BAD_LENGTH, "a length outside its table"),
                                    (BAD_OFFSETS, "row offsets that decrease or leave the rows")) if bits & b]

@@ -81,3 +81,17 @@ def test_attend_one_long_sequence_among_many():
     s = Setup([40] * 63 + [500], [1] * 63 + [500], heads=8, d=64, page=64)
     check_attend(s, 8, BF16)
     check_attend(s, 32, BF16, window=30, sinks=3)
+
+
+def test_check_waits_for_other_streams():
+    s = Setup([20, 20], [1, 1], heads=1, d=64)
+    x = torch.zeros(2, 1, 64, device="cuda", dtype=BF16)
+    bad = torch.full((2, 2), -1, dtype=torch.int32, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)           # some milliseconds at least, of which check() knows nothing
+        s.cache.append(x, x, bad, s.lens)
+    with pytest.raises(ValueError, match="page"):
+        s.cache.check()
+    s.cache.check()                             # cleared
