@@ -95,3 +95,19 @@ def test_check_waits_for_other_streams():
     with pytest.raises(ValueError, match="page"):
         s.cache.check()
     s.cache.check()                             # cleared
+
+
+@pytest.mark.parametrize("rows,first", [(600, 0), (600, 300), (1, 0), (37, 36)])
+@pytest.mark.parametrize("d,counts", [(64, (1, 1)), (128, (20, 3)), (256, (70, 2))])
+def test_attend_padded_batch(d, counts, rows, first):
+    # `first` rows before the sequences and rows - first behind them, as a graph's fixed number of rows has
+    s = Setup([90, 400], counts, heads=2, d=d, page=32, seed=d)
+    q = torch.randn(s.total + rows, 6, d, generator=s.g).to(BF16).cuda()
+    mine = slice(first, first + s.total)
+    want = s.cache.attend(q[mine], s.table, s.lens, s.cu, max_q=max(counts))
+    torch.empty(q.shape, dtype=q.dtype, device="cuda").fill_(float("nan"))       # what the results' memory may have held
+    out, lse = s.cache.attend(q, s.table, s.lens, s.cu + first, max_q=max(counts))
+    assert torch.equal(out[mine], want[0]) and torch.equal(lse[mine], want[1])
+    for part in (slice(0, first), slice(first + s.total, None)):
+        assert (out[part] == 0).all() and (lse[part] == -math.inf).all()
+    s.cache.check()
