@@ -33,7 +33,8 @@
  *     [0, num_pages), a length outside the table and offsets that decrease or leave [0, total]
  *     set a bit of *status.  Such a page is never read or written: its tokens are left out of
  *     append and of attention, read as NaN and evicted as zeros; a length is cut to the table's.
- *   - Two sequences may share pages that are only read.
+ *   - Sequences may share pages in attend, read and weigh; append and evict write to pages that no
+ *     other sequence of the call has.
  */
 #ifndef SPLITZIP_KV4_H
 #define SPLITZIP_KV4_H
@@ -137,7 +138,8 @@ int splitzip_kv4_attend(const splitzip_kv4_cache *cache, const splitzip_kv4_batc
  * Adds to the weight of every token and KV head the attention it got: the sum over the queries
  * and the heads of the group of exp(scale q.k - lse), for queries that see the token.  lse f32
  * [total][q_heads] is what splitzip_kv4_attend gave for these queries; one of -infinity adds
- * nothing.  No two sequences of a call may share a page here.
+ * nothing.  A page that sequences share gets the sum over all of them, added in no fixed order (its
+ * last bits may differ from call to call); elsewhere results do not depend on timing.
  */
 int splitzip_kv4_weigh(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch,
                        const splitzip_kv4_queries *queries, const float *lse, void *stream);

@@ -3,12 +3,14 @@
 //   w_j += sum over the rows i (queries and heads of the group) that see j of 2^(x_ij - lse_i)
 //
 // with x and lse as powers of two.  The rows' sums are known, so each token's sum stands alone:
-// a wave owns its tokens, adds over all rows in 32 bits in a fixed order, and writes each weight
-// once; no atomics.  Scores are products with rows as the result's rows, so a lane holds four
+// a wave owns its tokens of a sequence, adds over the rows in 32 bits in a fixed order, and then adds to
+// each weight by one atomic (step_kernel: one for every 16 rows, in their order).  Atomics make the sum
+// right where sequences share pages, in an order that is not fixed there; elsewhere a weight has one
+// adder and results do not depend on timing.  They take the time that plain stores took.  Scores are products with rows as the result's rows, so a lane holds four
 // rows of one token and a sum over rows stays in the lane but for one exchange at the end.
 //
 // step_kernel: up to 16 rows a sequence and KV head.  The rows' operands stay in registers while
-// a wave runs over 64 tokens a turn, with the codes and weights of the next two turns on their way to
+// a wave runs over 64 tokens a turn, with the codes of the next two turns on their way to
 // LDS.  K's 68 bytes a token at D = 128 and 8 of weights: 64 steps of 128 .. 8192 tokens move 200 MB in
 // 52 us (3.8 TB/s; 57 us with one turn ahead in registers, 74 us with 16 tokens a turn), of which the
 // kernel takes 47: short sequences end before their ring is full.
@@ -43,12 +45,12 @@ template <int D>
 constexpr int kWeighTokens = weigh_tokens(D);
 
 // One turn of a wave in LDS, 64 tokens: K's codes of four groups (8 D bytes each: D >= 128 16 bytes a
-// lane in lane order, D = 256 two of them; D = 64 as in the cache), their scales (D = 64 as in the
-// cache, else 4 bytes a token, D = 256 two such runs) and the tokens' weights.
+// lane in lane order, D = 256 two of them; D = 64 as in the cache) and their scales (D = 64 as in the
+// cache, else 4 bytes a token, D = 256 two such runs).
 template <int D>
 struct Turn {
-    static constexpr int kCodes = 8 * D, kScales = 4 * kCodes, kWeights = kScales + 2 * D, kBytes = kWeights + 256;
-    static constexpr int kLoads = D == 64 ? 4 : D == 128 ? 6 : 11;       // instructions
+    static constexpr int kCodes = 8 * D, kScales = 4 * kCodes, kBytes = kScales + 2 * D;
+    static constexpr int kLoads = D == 64 ? 3 : D == 128 ? 5 : 10;       // instructions
 };
 
 // Groups g on pages `page` (-1: page 0's tokens) to a slot; t: the lane's token 16 (lane / 16) +
@@ -81,34 +83,31 @@ __device__ __forceinline__ void send_turn(const Cache &c, const int (&page)[4], 
         for (int i = 0; i < D / 128; ++i)
             to_lds4(c.k_scales + t * (D / 32) + 4 * i, slot + L::kScales + 256 * i);
     }
-    to_lds4((const uint8_t *)(c.weights + t), slot + L::kWeights);
 }
 
 // A slot's turn to registers, once its loads are done: all but the Younger instructions behind them.
 template <int D, int Younger>
-__device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KRaw<D> (&k)[4], float &w)
+__device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KRaw<D> (&k)[4])
 {
     typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
     typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
     const uint32_t r = lane & 15, quad = lane >> 4;
-    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)slot, own = base + 4 * lane;
+    const uint32_t base = (uint32_t)(uintptr_t)(lds_ptr)slot;
     if constexpr (D == 64) {
         const uint32_t at = base + r * 32 + quad * 8, ks = base + r * 2 + (quad >> 1);
         u32x2 a, b, c, d;
-        asm volatile("s_waitcnt vmcnt(%12)\n"
-                     "ds_read_b64 %0, %9\n"
-                     "ds_read_b64 %1, %9 offset:512\n"
-                     "ds_read_b64 %2, %9 offset:1024\n"
-                     "ds_read_b64 %3, %9 offset:1536\n"
-                     "ds_read_u8 %4, %10 offset:2048\n"
-                     "ds_read_u8 %5, %10 offset:2080\n"
-                     "ds_read_u8 %6, %10 offset:2112\n"
-                     "ds_read_u8 %7, %10 offset:2144\n"
-                     "ds_read_b32 %8, %11 offset:2176\n"
+        asm volatile("s_waitcnt vmcnt(%10)\n"
+                     "ds_read_b64 %0, %8\n"
+                     "ds_read_b64 %1, %8 offset:512\n"
+                     "ds_read_b64 %2, %8 offset:1024\n"
+                     "ds_read_b64 %3, %8 offset:1536\n"
+                     "ds_read_u8 %4, %9 offset:2048\n"
+                     "ds_read_u8 %5, %9 offset:2080\n"
+                     "ds_read_u8 %6, %9 offset:2112\n"
+                     "ds_read_u8 %7, %9 offset:2144\n"
                      "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s),
-                       "=&v"(w)
-                     : "v"(at), "v"(ks), "v"(own), "n"(Younger)
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s)
+                     : "v"(at), "v"(ks), "n"(Younger)
                      : "memory");
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -117,20 +116,18 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
     } else if constexpr (D == 128) {
         const uint32_t at = base + 16 * lane, ks = base + r * 4 + quad;
         u32x4 a, b, c, d;
-        asm volatile("s_waitcnt vmcnt(%12)\n"
-                     "ds_read_b128 %0, %9\n"
-                     "ds_read_b128 %1, %9 offset:1024\n"
-                     "ds_read_b128 %2, %9 offset:2048\n"
-                     "ds_read_b128 %3, %9 offset:0xc00\n"
-                     "ds_read_u8 %4, %10 offset:4096\n"
-                     "ds_read_u8 %5, %10 offset:4160\n"
-                     "ds_read_u8 %6, %10 offset:4224\n"
-                     "ds_read_u8 %7, %10 offset:4288\n"
-                     "ds_read_b32 %8, %11 offset:4352\n"
+        asm volatile("s_waitcnt vmcnt(%10)\n"
+                     "ds_read_b128 %0, %8\n"
+                     "ds_read_b128 %1, %8 offset:1024\n"
+                     "ds_read_b128 %2, %8 offset:2048\n"
+                     "ds_read_b128 %3, %8 offset:0xc00\n"
+                     "ds_read_u8 %4, %9 offset:4096\n"
+                     "ds_read_u8 %5, %9 offset:4160\n"
+                     "ds_read_u8 %6, %9 offset:4224\n"
+                     "ds_read_u8 %7, %9 offset:4288\n"
                      "s_waitcnt lgkmcnt(0)"
-                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s),
-                       "=&v"(w)
-                     : "v"(at), "v"(ks), "v"(own), "n"(Younger)
+                     : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s)
+                     : "v"(at), "v"(ks), "n"(Younger)
                      : "memory");
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -139,24 +136,23 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
     } else {
         const uint32_t at = base + 16 * lane, ks = base + r * 4 + (quad >> 1) * 256 + (quad & 1) * 2;
         u32x4 a, b, c, d, e, f, g, h;
-        asm volatile("s_waitcnt vmcnt(%16)\n"
-                     "ds_read_b128 %0, %13\n"
-                     "ds_read_b128 %1, %13 offset:1024\n"
-                     "ds_read_b128 %2, %13 offset:2048\n"
-                     "ds_read_b128 %3, %13 offset:0xc00\n"
-                     "ds_read_b128 %4, %13 offset:4096\n"
-                     "ds_read_b128 %5, %13 offset:5120\n"
-                     "ds_read_b128 %6, %13 offset:6144\n"
-                     "ds_read_b128 %7, %13 offset:7168\n"
-                     "ds_read_u16 %8, %14 offset:8192\n"
-                     "ds_read_u16 %9, %14 offset:8256\n"
-                     "ds_read_u16 %10, %14 offset:8320\n"
-                     "ds_read_u16 %11, %14 offset:8384\n"
-                     "ds_read_b32 %12, %15 offset:8704\n"
+        asm volatile("s_waitcnt vmcnt(%14)\n"
+                     "ds_read_b128 %0, %12\n"
+                     "ds_read_b128 %1, %12 offset:1024\n"
+                     "ds_read_b128 %2, %12 offset:2048\n"
+                     "ds_read_b128 %3, %12 offset:0xc00\n"
+                     "ds_read_b128 %4, %12 offset:4096\n"
+                     "ds_read_b128 %5, %12 offset:5120\n"
+                     "ds_read_b128 %6, %12 offset:6144\n"
+                     "ds_read_b128 %7, %12 offset:7168\n"
+                     "ds_read_u16 %8, %13 offset:8192\n"
+                     "ds_read_u16 %9, %13 offset:8256\n"
+                     "ds_read_u16 %10, %13 offset:8320\n"
+                     "ds_read_u16 %11, %13 offset:8384\n"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(k[0].s),
-                       "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s), "=&v"(w)
-                     : "v"(at), "v"(ks), "v"(own), "n"(Younger)
+                       "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s)
+                     : "v"(at), "v"(ks), "n"(Younger)
                      : "memory");
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -239,8 +235,6 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
             send_turn<D>(a.c, page, head, g, t, lane, sh_turn[wave][i & 1]);
             return mine < 0 || 16 * mine_g + r >= q.len ? nullptr : a.c.weights + t;
         };
-        if (row0 > 0)
-            __threadfence();             // the rows before have written the weights
         float *at0 = nullptr, *at1 = nullptr;
         if (turns > 0)
             at0 = send(0);
@@ -248,11 +242,10 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
             at1 = send(1);
         for (int i = 0; i < turns; ++i) {
             KRaw<D> k[4];
-            float w;
             if (i + 1 < turns)
-                take_turn<D, Turn<D>::kLoads>(sh_turn[wave][i & 1], lane, k, w);
+                take_turn<D, Turn<D>::kLoads>(sh_turn[wave][i & 1], lane, k);
             else
-                take_turn<D, 0>(sh_turn[wave][i & 1], lane, k, w);
+                take_turn<D, 0>(sh_turn[wave][i & 1], lane, k);
             float *const at = at0;
             at0 = at1;
             if (i + 2 < turns)
@@ -285,7 +278,7 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
                 mine = quad == e ? sum : mine;
             }
             if (at)
-                *at = w + mine;
+                unsafeAtomicAdd(at, mine);
         }
     }
 }
@@ -486,8 +479,7 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
         for (int n = 0; n < kTiles; ++n) {
             const float all = half_sum(sum[n]);
             if (page[n] >= 0 && half == 0) {
-                float *w = a.c.weights + group_first(a.c, page[n], head, token[n] >> 4) + (token[n] & 15);
-                *w += all;
+                unsafeAtomicAdd(a.c.weights + group_first(a.c, page[n], head, token[n] >> 4) + (token[n] & 15), all);
             }
         }
     }

@@ -255,7 +255,7 @@ class KV4Cache:
     def weigh(self, q, lse, table, lens, cu=None, max_q=None, max_len=None, scale=None, window=None, sinks=0):
         """Adds to ``weights`` the attention that every token and KV head got from q: exp(scale q.k - lse)
         over the queries that see it and the heads of its group.  ``lse`` is what ``attend`` gave
-        for these queries and masks."""
+        for these queries and masks.  Pages that sequences share get the sum over all of them."""
         qs = self._queries(q, scale, window, sinks)
         if lse.dtype is not self._f32 or tuple(lse.shape) != tuple(q.shape[:2]) or not lse.is_contiguous() or \
                 lse.device != self.device:

@@ -111,3 +111,21 @@ def test_attend_padded_batch(d, counts, rows, first):
     for part in (slice(0, first), slice(first + s.total, None)):
         assert (out[part] == 0).all() and (lse[part] == -math.inf).all()
     s.cache.check()
+
+
+@pytest.mark.parametrize("counts,group", [((1,) * 12, 8), ((5,) * 12, 8), ((40,) * 12, 3)])
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (128, FP16), (256, BF16)])
+def test_weigh_shared_pages(d, dtype, counts, group):
+    # twelve sequences of one prefix: what its pages get is the sum over all of them
+    s = Setup([300, *range(200, 310, 10)], counts, heads=2, d=d, page=32, seed=d)
+    for q in range(1, 12):
+        s.table_h[q, :6] = s.table_h[0, :6]
+    s.table = s.table_h.cuda()
+    q = s.queries(2 * group, dtype)
+    for mask in ({"window": None, "sinks": 0}, {"window": 150, "sinks": 40}):
+        _, lse = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, **mask)
+        s.cache.weights.nan_to_num_(0.25)
+        r = ref.Cache(s.cache)
+        s.cache.weigh(q.cuda(), lse, s.table, s.lens, s.cu, max_q=max(counts), **mask)
+        w, tol = ref.weigh(r, q.double(), lse.cpu().double(), s.rows(), s.lens_l, s.counts, d ** -0.5, mask["window"], mask["sinks"])
+        assert ((s.cache.weights.cpu().double() - w).abs() <= tol + 12 * ref.U32 * w.abs()).all()
