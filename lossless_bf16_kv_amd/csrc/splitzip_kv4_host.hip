@@ -100,7 +100,9 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
     // kernels count up to 256 rows past a sequence's last in 32 bits
     KV4_REQUIRE(b->total * q->q_heads <= INT32_MAX - 65536, "total * q_heads must be below 2^31 - 65536");
     KV4_REQUIRE(q->window >= 0 && q->sinks >= 0, "window or sinks is negative");
-    KV4_REQUIRE(std::isfinite(q->scale), "scale is not finite");
+    // scores are held as powers of two
+    const float scale2 = (float)((double)q->scale * 1.4426950408889634);
+    KV4_REQUIRE(std::isfinite(scale2), "scale is not finite, or scale * log2(e) is not");
     KV4_REQUIRE(q->q || b->total == 0, "q is null");
     KV4_REQUIRE((reinterpret_cast<uintptr_t>(q->q) & 1) == 0, "q is not aligned to its type");
     a->q = q->q;
@@ -110,7 +112,7 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
     a->group = q->q_heads / c->kv_heads;
     a->window = q->window;
     a->sinks = q->sinks;
-    a->scale2 = (float)((double)q->scale * 1.4426950408889634);
+    a->scale2 = scale2;
     a->wide = aligned16(q->q) && q->token_stride % 8 == 0 && q->head_stride % 8 == 0;
     return SPLITZIP_OK;
 }

@@ -1,5 +1,5 @@
-"""CPU tests of what the 4-bit KV cache's calls launch, and of what they refuse because no launch holds it.  No call
-here reaches the GPU."""
+"""CPU tests of what the 4-bit KV cache's calls launch, and of what they refuse because no launch or 32-bit number
+holds it.  No call here reaches the GPU."""
 from __future__ import annotations
 
 import ctypes
@@ -184,3 +184,10 @@ def test_python_hint_past_32_bits_is_not_cut(max_q):
     me = types.SimpleNamespace(page_size=16, _int32=lambda t, name, shape=None: 0)
     assert kv4.KV4Cache._batch(me, t, t, t, 300, max_q, None).max_q == MOST
     assert kv4.KV4Cache._batch(me, t, t, t, 300, None, max_q).max_len == MOST
+
+
+@pytest.mark.parametrize("op", ["attend", "weigh"])
+@pytest.mark.parametrize("scale", [3e38, -3e38, 2.4e38])
+def test_scale_that_is_infinite_in_base_2(op, scale):
+    # scores are held as powers of two: scale * log2(e) must be a 32-bit number too
+    refused(op, "scale is not finite", q=queries(scale=scale))
