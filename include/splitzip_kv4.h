@@ -91,6 +91,8 @@ typedef struct splitzip_kv4_batch {
  * Queries [total][q_heads][head_dim] with strides in elements (channels adjacent).  Query head
  * f reads KV head f / (q_heads / kv_heads).  Query i of a sequence stands at token
  * p = len - n + i and sees tokens j <= p with j > p - window or j < sinks; window 0: no window.
+ * scale 0: attend counts all of them alike, whatever the query holds; weigh gives NaN for a query
+ * that is not finite.
  */
 typedef struct splitzip_kv4_queries {
     const void *q;

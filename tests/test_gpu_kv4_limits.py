@@ -129,3 +129,28 @@ def test_weigh_shared_pages(d, dtype, counts, group):
         s.cache.weigh(q.cuda(), lse, s.table, s.lens, s.cu, max_q=max(counts), **mask)
         w, tol = ref.weigh(r, q.double(), lse.cpu().double(), s.rows(), s.lens_l, s.counts, d ** -0.5, mask["window"], mask["sinks"])
         assert ((s.cache.weights.cpu().double() - w).abs() <= tol + 12 * ref.U32 * w.abs()).all()
+
+
+@pytest.mark.parametrize("counts", [(1, 1), (7, 3), (40, 90)])
+@pytest.mark.parametrize("d,dtype", [(64, FP16), (128, BF16), (256, BF16)])
+@pytest.mark.parametrize("scale", [0.1, -0.1])
+def test_queries_that_are_not_finite(d, dtype, counts, scale):
+    s = Setup([90, 130], counts, heads=2, d=d, page=32, seed=d)
+    q = s.queries(4, dtype)
+    q[0, 0, 3], q[1, 1, d - 1], q[-1, 2, 17], q[-1, 3, d // 2] = math.inf, -math.inf, math.nan, math.inf
+    out, lse = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, scale=scale)
+    eo, to, el, tl = ref.attend(ref.Cache(s.cache), q.double(), s.rows(), s.lens_l, s.counts, scale, None, 0, dtype)
+    out, lse = out.cpu().double(), lse.cpu().double()
+    assert el.isnan().any() and torch.equal(lse.isnan(), el.isnan()) and torch.equal(out.isnan(), eo.isnan())
+    assert ((out - eo).abs() <= to)[~eo.isnan()].all() and ((lse - el).abs() <= tl)[~el.isnan()].all()
+
+
+@pytest.mark.parametrize("counts", [(1, 1), (40, 90)])
+def test_scale_of_0_leaves_the_queries_out(counts):
+    # every token that a query sees counts alike, whatever the query holds
+    s = Setup([90, 130], counts, heads=2, d=64, page=32)
+    q = s.queries(4, BF16)
+    q[0, 0, 3], q[-1, 2, 17] = math.inf, math.nan
+    out, lse = check_attend(s, 4, BF16, scale=0.0, q=q.nan_to_num(0.0, 1.0, 1.0))[1:]
+    got = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, scale=0.0)
+    assert torch.equal(got[0].cpu().double(), out) and torch.equal(got[1].cpu().double(), lse)
