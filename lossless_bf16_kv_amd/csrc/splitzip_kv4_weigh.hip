@@ -98,13 +98,13 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
         u32x2 a, b, c, d;
         asm volatile("s_waitcnt vmcnt(%10)\n"
                      "ds_read_b64 %0, %8\n"
-                     "ds_read_b64 %1, %8 offset:512\n"
-                     "ds_read_b64 %2, %8 offset:1024\n"
-                     "ds_read_b64 %3, %8 offset:1536\n"
-                     "ds_read_u8 %4, %9 offset:2048\n"
-                     "ds_read_u8 %5, %9 offset:2080\n"
-                     "ds_read_u8 %6, %9 offset:2112\n"
-                     "ds_read_u8 %7, %9 offset:2144\n"
+                     "ds_read_b64 %1, %8 offset:0x200\n"
+                     "ds_read_b64 %2, %8 offset:0x400\n"
+                     "ds_read_b64 %3, %8 offset:0x600\n"
+                     "ds_read_u8 %4, %9 offset:0x800\n"
+                     "ds_read_u8 %5, %9 offset:0x820\n"
+                     "ds_read_u8 %6, %9 offset:0x840\n"
+                     "ds_read_u8 %7, %9 offset:0x860\n"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s)
                      : "v"(at), "v"(ks), "n"(Younger)
@@ -118,13 +118,13 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
         u32x4 a, b, c, d;
         asm volatile("s_waitcnt vmcnt(%10)\n"
                      "ds_read_b128 %0, %8\n"
-                     "ds_read_b128 %1, %8 offset:1024\n"
-                     "ds_read_b128 %2, %8 offset:2048\n"
+                     "ds_read_b128 %1, %8 offset:0x400\n"
+                     "ds_read_b128 %2, %8 offset:0x800\n"
                      "ds_read_b128 %3, %8 offset:0xc00\n"
-                     "ds_read_u8 %4, %9 offset:4096\n"
-                     "ds_read_u8 %5, %9 offset:4160\n"
-                     "ds_read_u8 %6, %9 offset:4224\n"
-                     "ds_read_u8 %7, %9 offset:4288\n"
+                     "ds_read_u8 %4, %9 offset:0x1000\n"
+                     "ds_read_u8 %5, %9 offset:0x1040\n"
+                     "ds_read_u8 %6, %9 offset:0x1080\n"
+                     "ds_read_u8 %7, %9 offset:0x10c0\n"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(k[0].s), "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s)
                      : "v"(at), "v"(ks), "n"(Younger)
@@ -138,17 +138,17 @@ __device__ __forceinline__ void take_turn(const uint8_t *slot, uint32_t lane, KR
         u32x4 a, b, c, d, e, f, g, h;
         asm volatile("s_waitcnt vmcnt(%14)\n"
                      "ds_read_b128 %0, %12\n"
-                     "ds_read_b128 %1, %12 offset:1024\n"
-                     "ds_read_b128 %2, %12 offset:2048\n"
+                     "ds_read_b128 %1, %12 offset:0x400\n"
+                     "ds_read_b128 %2, %12 offset:0x800\n"
                      "ds_read_b128 %3, %12 offset:0xc00\n"
-                     "ds_read_b128 %4, %12 offset:4096\n"
-                     "ds_read_b128 %5, %12 offset:5120\n"
-                     "ds_read_b128 %6, %12 offset:6144\n"
-                     "ds_read_b128 %7, %12 offset:7168\n"
-                     "ds_read_u16 %8, %13 offset:8192\n"
-                     "ds_read_u16 %9, %13 offset:8256\n"
-                     "ds_read_u16 %10, %13 offset:8320\n"
-                     "ds_read_u16 %11, %13 offset:8384\n"
+                     "ds_read_b128 %4, %12 offset:0x1000\n"
+                     "ds_read_b128 %5, %12 offset:0x1400\n"
+                     "ds_read_b128 %6, %12 offset:0x1800\n"
+                     "ds_read_b128 %7, %12 offset:0x1c00\n"
+                     "ds_read_u16 %8, %13 offset:0x2000\n"
+                     "ds_read_u16 %9, %13 offset:0x2040\n"
+                     "ds_read_u16 %10, %13 offset:0x2080\n"
+                     "ds_read_u16 %11, %13 offset:0x20c0\n"
                      "s_waitcnt lgkmcnt(0)"
                      : "=&v"(a), "=&v"(b), "=&v"(c), "=&v"(d), "=&v"(e), "=&v"(f), "=&v"(g), "=&v"(h), "=&v"(k[0].s),
                        "=&v"(k[1].s), "=&v"(k[2].s), "=&v"(k[3].s)
