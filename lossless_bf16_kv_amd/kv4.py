@@ -13,6 +13,8 @@ A call's sequences are given by ``table`` (int32 [seqs, pages], the page numbers
 sequence in q, k, v; None: one row a sequence).  A sequence's n rows stand at its last n tokens.
 They live on the GPU; values out of range are caught there and reported by ``check``.
 
+Nothing here is differentiable: results carry no gradient, also where inputs require one.
+
     cache = kv4.KV4Cache(num_pages=4096, page_size=64, kv_heads=8, head_dim=128)
     cache.append(k, v, table, lens, cu)
     out, lse = cache.attend(q, table, lens, cu, max_q=longest, window=4096, sinks=4)

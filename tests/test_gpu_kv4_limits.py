@@ -154,3 +154,14 @@ def test_scale_of_0_leaves_the_queries_out(counts):
     out, lse = check_attend(s, 4, BF16, scale=0.0, q=q.nan_to_num(0.0, 1.0, 1.0))[1:]
     got = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, scale=0.0)
     assert torch.equal(got[0].cpu().double(), out) and torch.equal(got[1].cpu().double(), lse)
+
+
+def test_results_carry_no_gradient():
+    s = Setup([20, 9], [1, 1], heads=1, d=64)
+    q = s.queries(2, BF16).cuda().requires_grad_()
+    k = torch.randn(2, 1, 64, generator=s.g).cuda().requires_grad_()
+    s.cache.append(k, k, s.table, s.lens)
+    out, lse = s.cache.attend(q, s.table, s.lens)
+    assert not out.requires_grad and not lse.requires_grad
+    want = s.cache.attend(q.detach(), s.table, s.lens)
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
