@@ -984,7 +984,8 @@ hipError_t attend_d(const AttendArgs &a, int dtype, hipStream_t s)
 
 // Few rows wait for nobody, and waste no products on rows that are not there: drafts of 12 to 24 rows take
 // 34 us by few_rows and 79 us in a tile of 64, decode steps of 8 rows 41 and 92 us.  More rows pay for a
-// shared conversion: 16384 rows 672 us by 64, 511 by 128, 419 by 256.  At 256 channels 32 rows by few_rows
+// shared conversion: 16384 rows 672 us by 64, 511 by 128, 419 by 256; in fp16 701 by 128 and 661 by 256, though that
+// one spills 5 registers at 128 channels.  At 256 channels 32 rows by few_rows
 // and 256 by many_rows would not leave room for two waves' registers.
 int attend_rows(int head_dim, int64_t rows)
 {
