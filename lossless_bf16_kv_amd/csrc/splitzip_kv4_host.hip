@@ -177,17 +177,21 @@ int plan_weigh(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, AttendA
     const int64_t pairs = (int64_t)b->n_seqs * c->kv_heads;
     KV4_REQUIRE(pairs <= 1 << 22, "more than 2^22 sequences and heads");
     const int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
-    const int64_t rows = expected_rows(*b, a->group);
-    // Up to 16 rows stay in registers: 64 decode steps of 8 rows 52 us, by rows_kernel 135.
-    a->tile_rows = rows <= kStepRows ? kStepRows : 0;
-    if (a->tile_rows == kStepRows) {
-        // 256 tokens a workgroup at least (one turn of each wave), and 2048 workgroups at most (the same at
-        // 4096; 1024 took 63 us for 57)
+    // Up to 16 rows stay in registers: 64 decode steps of 8 rows 52 us, by rows_kernel 135.  Where the mean is up to
+    // 16 and nobody says what the longest has, step_kernel takes the sequences of up to 16 and a second
+    // launch of up to 8192 workgroups the others: 256 decode steps of 8 rows 187 us, all by rows_kernel 499; 255 of them
+    // and a prompt of 512 queries 503, all by rows_kernel 548, by step_kernel 2474.
+    const bool few = expected_rows(*b, a->group) <= kStepRows, more = !few || b->max_q == 0;
+    a->splits = a->row_splits = 0;
+    // 256 tokens a workgroup at least (one turn of each wave), and 2048 workgroups at most (the same at 4096;
+    // 1024 took 63 us for 57)
+    if (few)
         a->splits = (int32_t)std::min<int64_t>(std::max<int64_t>(1, 2048 / pairs), tokens / 256 + 1);
-    } else {
-        // a launch that would be too large has fewer, which take tokens in turn
-        a->splits = (int32_t)std::min(tokens / weigh_tokens(c->head_dim) + 1, kMostThreads / kWeighThreads / pairs);
-    }
+    // a launch that would be too large has fewer, which take tokens in turn
+    const int64_t most = few ? std::max<int64_t>(1, 8192 / pairs) : kMostThreads / kWeighThreads / pairs;
+    a->step_rows = !few ? 0 : more ? kStepRows : INT32_MAX;
+    if (more)
+        a->row_splits = (int32_t)std::min(tokens / weigh_tokens(c->head_dim) + 1, most);
     return SPLITZIP_OK;
 }
 
@@ -329,8 +333,7 @@ int splitzip_kv4_weigh(const splitzip_kv4_cache *cache, const splitzip_kv4_batch
     Device d(cache->device);
     if (d.status)
         return d.status;
-    launch_weigh(a, cache->head_dim, queries->dtype, static_cast<hipStream_t>(stream));
-    return Device::launched();
+    return Device::launched(launch_weigh(a, cache->head_dim, queries->dtype, static_cast<hipStream_t>(stream)));
 }
 
 int splitzip_kv4_evict(const splitzip_kv4_cache *cache, const splitzip_kv4_batch *batch, const int32_t *out_table,
@@ -405,8 +408,12 @@ int splitzip_kv4_launches(int32_t op, const splitzip_kv4_cache *cache, const spl
     if (op == SPLITZIP_KV4_WEIGH) {
         if (int e = plan_weigh(cache, batch, &a))
             return e;
-        workgroups[0] = (uint64_t)a.b.n_seqs * a.c.heads * a.splits;
-        threads[0] = kWeighThreads;
+        for (int32_t splits : {a.splits, a.row_splits})
+            if (splits > 0) {
+                const int i = threads[0] ? 1 : 0;
+                workgroups[i] = (uint64_t)a.b.n_seqs * a.c.heads * splits;
+                threads[i] = kWeighThreads;
+            }
         return SPLITZIP_OK;
     }
     if (int e = plan(cache, batch, queries, &a))

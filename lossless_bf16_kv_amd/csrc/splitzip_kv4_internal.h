@@ -54,7 +54,10 @@ struct AttendArgs {
     const float *lse_in;     // weigh
     float *part_o, *part_ml; // partial results of splits > 1: [split][row][D], [split][row][2]
     int32_t splits, tiles;   // workgroups along the tokens and along the rows of a sequence and head
-    int32_t per, tile_rows;  // attend: groups of 16 tokens a split, rows a tile; weigh: rows a tile, 0: no tiles
+    int32_t per, tile_rows;  // attend: groups of 16 tokens a split, rows a tile
+    // weigh: workgroups along the tokens of rows_kernel (`splits`: of step_kernel; 0: not launched), and how many rows
+    // a sequence has at most that is left to step_kernel
+    int32_t row_splits, step_rows;
 };
 
 struct EvictArgs {
@@ -80,7 +83,7 @@ int join_rows(int head_dim);                   // rows of a workgroup of join_ke
 constexpr int kJoinThreads = 256, kWeighThreads = 256, kStepRows = 16;
 constexpr int weigh_tokens(int head_dim) { return head_dim == 256 ? 128 : 256; }     // of a workgroup of rows_kernel
 hipError_t launch_attend(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
-void launch_weigh(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
+hipError_t launch_weigh(const AttendArgs &a, int head_dim, int dtype, hipStream_t s);
 hipError_t launch_evict(const EvictArgs &a, int head_dim, hipStream_t s);
 
 // ---- device ---------------------------------------------------------------------------------

@@ -178,7 +178,7 @@ __global__ __launch_bounds__(kLanes, 2) void step_kernel(AttendArgs a)
     const int rows = q.n * a.group;
     const Mask mask = {a.window, a.sinks};
     const int base = q.len - q.n;
-    if (rows == 0)
+    if (rows == 0 || rows > a.step_rows)
         return;
     // groups that some row sees; each wave keeps its own over all rows, 16 of which go at a time
     const Groups groups(base, q.len - 1, a.window, a.sinks);
@@ -306,9 +306,9 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
     const Seq q = wave_sequence(a.c, a.b, s);
     const int rows = q.n * a.group, base = q.len - q.n;
     const Mask mask = {a.window, a.sinks};
-    const int len = rows > 0 ? q.len : 0;
+    const int len = rows > a.step_rows ? q.len : 0;
 
-    for (int64_t j00 = (int64_t)split * kWeighTokens<D>; j00 < len; j00 += (int64_t)a.splits * kWeighTokens<D>) {
+    for (int64_t j00 = (int64_t)split * kWeighTokens<D>; j00 < len; j00 += (int64_t)a.row_splits * kWeighTokens<D>) {
         const int j0 = (int)j00, j1 = (int)min(j00 + kWeighTokens<D>, (int64_t)q.len) - 1;   // the workgroup's tokens
         // rows that see one of them: queries from j0, up to the window's end unless always visible
         const int64_t past = a.window > 0 && j0 >= a.sinks ? (int64_t)j1 + a.window - 1 : (int64_t)q.len;
@@ -485,27 +485,30 @@ __global__ __launch_bounds__(kLanes, 2) void rows_kernel(AttendArgs a)
     }
 }
 
+// Where both are launched, each takes the sequences that it is made for.
 template <int D, int T>
-void weigh_dt(const AttendArgs &a, hipStream_t s)
+hipError_t weigh_dt(const AttendArgs &a, hipStream_t s)
 {
-    const unsigned grid = (unsigned)((int64_t)a.b.n_seqs * a.c.heads * a.splits);
-    if (a.tile_rows == kStepRows)
-        step_kernel<D, T><<<grid, kLanes, 0, s>>>(a);
-    else
-        rows_kernel<D, T><<<grid, kLanes, 0, s>>>(a);
+    const int64_t pairs = (int64_t)a.b.n_seqs * a.c.heads;
+    if (a.splits > 0)
+        step_kernel<D, T><<<(unsigned)(pairs * a.splits), kLanes, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.row_splits == 0)
+        return e;
+    rows_kernel<D, T><<<(unsigned)(pairs * a.row_splits), kLanes, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-void launch_weigh(const AttendArgs &a, int head_dim, int dtype, hipStream_t s)
+hipError_t launch_weigh(const AttendArgs &a, int head_dim, int dtype, hipStream_t s)
 {
     const bool b = dtype == SPLITZIP_KV4_BF16;
     if (head_dim == 64)
-        b ? weigh_dt<64, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<64, SPLITZIP_KV4_FP16>(a, s);
-    else if (head_dim == 128)
-        b ? weigh_dt<128, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<128, SPLITZIP_KV4_FP16>(a, s);
-    else
-        b ? weigh_dt<256, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<256, SPLITZIP_KV4_FP16>(a, s);
+        return b ? weigh_dt<64, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<64, SPLITZIP_KV4_FP16>(a, s);
+    if (head_dim == 128)
+        return b ? weigh_dt<128, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<128, SPLITZIP_KV4_FP16>(a, s);
+    return b ? weigh_dt<256, SPLITZIP_KV4_BF16>(a, s) : weigh_dt<256, SPLITZIP_KV4_FP16>(a, s);
 }
 
 }  // namespace kv4

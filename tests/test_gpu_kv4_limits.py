@@ -165,3 +165,21 @@ def test_results_carry_no_gradient():
     assert not out.requires_grad and not lse.requires_grad
     want = s.cache.attend(q.detach(), s.table, s.lens)
     assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("d,dtype", [(64, BF16), (128, FP16), (256, BF16)])
+def test_weigh_without_max_q(d, dtype):
+    # sequences of 4, 8, 16, 20 and 160 rows: the mean is below 16, and two kernels share them
+    counts = [1] * 30 + [2, 4, 5, 40, 0, 3]
+    s = Setup([30] * 30 + [90, 64, 70, 300, 5, 2], counts, heads=2, d=d, page=32, seed=d)
+    assert s.total * 4 <= 16 * len(counts)
+    q = s.queries(8, dtype)
+    for mask in ({"window": None, "sinks": 0}, {"window": 33, "sinks": 5}):
+        _, lse = s.cache.attend(q.cuda(), s.table, s.lens, s.cu, **mask)
+        r = ref.Cache(s.cache)
+        s.cache.weigh(q.cuda(), lse, s.table, s.lens, s.cu, **mask)
+        w, tol = ref.weigh(r, q.double(), lse.cpu().double(), s.rows(), s.lens_l, s.counts, d ** -0.5, mask["window"], mask["sinks"])
+        got = s.cache.weights.cpu().double()
+        assert torch.equal(got.isnan(), w.isnan())
+        ok = ~w.isnan()
+        assert ((got - w).abs()[ok] <= tol[ok]).all()

@@ -162,13 +162,13 @@ def test_attend_launch_without_max_q(seqs, n, group, threads, least):
 
 
 def test_weigh_launch_without_max_q():
-    # up to 16 rows a sequence stay in registers
+    # up to 16 rows a sequence stay in registers; a second launch is there for sequences that have more
     b = batch(n_seqs=64, total=192, cu_seqlens=1 << 20, table_width=64, table_stride=64, max_len=4096)
     got = []
     for max_q in (0, 3, 192):
         b.max_q = max_q
         got.append(launches(WEIGH, b=b, q=queries(q_heads=32, token_stride=4096)))
-    assert got[0] == got[1] != got[2]
+    assert got[0][:1] == got[1] != got[2] and len(got[0]) == 2 and got[0][1][0] <= 8192 and len(got[2]) == 1
 
 
 def test_python_says_that_it_does_not_know():
