@@ -143,15 +143,19 @@ int plan(const splitzip_kv4_cache *c, const splitzip_kv4_batch *b, const splitzi
     // workgroups that a launch holds; fewer tiles and splits than there could be take rows and tokens in turn
     const int64_t most = kMostThreads / attend_threads(c->head_dim, a->tile_rows);
     KV4_REQUIRE(pairs <= most, "too many sequences and heads");
-    // Without max_q a sequence may have more rows than expected, all of them at most: twice the tiles, up to 4096
-    // workgroups, and rows in turn beyond.  An odd number of tiles, since the ones with rows would meet on
-    // few CUs where it is a multiple of their number.  Against all rows as every sequence's (us): 64 requests
-    // of 3 drafts 83 for 489, 256 single tokens 238 for 4161, 16 prompts of 64 .. 4096 tokens 1044 for
-    // 1211, a prompt of 2048 among 63 single tokens 620 for 642; up to 16384 workgroups 107, 242, 1060, 645.
+    // Without max_q a sequence may have more rows than expected, all of them at most: twice the tiles, or 8 up to 16384
+    // workgroups, or what makes 4096, and rows in turn beyond.  An odd number of tiles, since the ones with
+    // rows would meet on few CUs where it is a multiple of their number.  Against all rows as every
+    // sequence's (us): 64 requests of 3 drafts 85 for 489, 256 single tokens 254 for 4190, 16 prompts of 64 ..
+    // 4096 tokens 1040 for 1211; a prompt of 2048 among 63 single tokens 614 for 642, among 255 2090 for
+    // 5400 (6030 with 4096 workgroups at most); the drafts with 16384 workgroups 107.
     const int64_t expected = ceil_div(rows, a->tile_rows);
     int64_t tiles = expected;
-    if (b->max_q == 0)
-        tiles = std::min(std::max(2 * expected, 4096 / std::max<int64_t>(1, pairs)), ceil_div(b->total * a->group, a->tile_rows)) | 1;
+    if (b->max_q == 0) {
+        const int64_t one = std::max<int64_t>(1, pairs);
+        tiles = std::max({2 * expected, std::min<int64_t>(8, 16384 / one), 4096 / one});
+        tiles = std::min(tiles, ceil_div(b->total * a->group, a->tile_rows)) | 1;
+    }
     tiles = std::min(tiles, most / std::max<int64_t>(1, pairs));
     int64_t tokens = std::min<int64_t>(b->max_len, (int64_t)b->table_width * c->page_size);
     if (q->window > 0)

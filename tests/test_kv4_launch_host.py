@@ -158,7 +158,7 @@ def test_attend_launch_without_max_q(seqs, n, group, threads, least):
     tiles = groups // (seqs * 8)
     assert got == threads and tiles >= least
     if seqs > 1:
-        assert groups <= max(4096 + seqs * 8, 3 * least * seqs * 8)
+        assert groups <= max(16384 + seqs * 8, 3 * least * seqs * 8)
 
 
 def test_weigh_launch_without_max_q():
