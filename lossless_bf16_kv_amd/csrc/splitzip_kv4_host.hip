@@ -97,8 +97,8 @@ int check_queries(const splitzip_kv4_queries *q, const splitzip_kv4_batch *b, co
     KV4_REQUIRE(q, "queries is null");
     KV4_REQUIRE(q->dtype == SPLITZIP_KV4_BF16 || q->dtype == SPLITZIP_KV4_FP16, "queries must be bf16 or fp16");
     KV4_REQUIRE(q->q_heads >= c->kv_heads && q->q_heads % c->kv_heads == 0, "q_heads must be a multiple of kv_heads");
-    // kernels count up to 256 rows past a sequence's last in 32 bits
-    KV4_REQUIRE(b->total * q->q_heads <= INT32_MAX - 65536, "total * q_heads must be below 2^31 - 65536");
+    // kernels count past a sequence's last row in 32 bits, by up to 4097 tiles of 32 rows (plan)
+    KV4_REQUIRE(b->total * q->q_heads < INT32_MAX - (1 << 18), "total * q_heads must be below 2^31 - 2^18");
     KV4_REQUIRE(q->window >= 0 && q->sinks >= 0, "window or sinks is negative");
     // scores are held as powers of two
     const float scale2 = (float)((double)q->scale * 1.4426950408889634);

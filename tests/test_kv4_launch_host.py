@@ -109,12 +109,13 @@ def test_append_and_read_of_too_many_rows(op, d, rows, heads):
     refused(op, "more rows and heads than a launch holds", c=cache(head_dim=d, kv_heads=heads), b=b)
 
 
-# The kernels count up to 256 rows past a sequence's last in 32 bits.
+# The kernels count past a sequence's last row in 32 bits: by 256 in tiles, by 4097 tiles of 32 where rows go in turn.
 @pytest.mark.parametrize("op", ["attend", "weigh"])
-@pytest.mark.parametrize("total,heads", [(MOST - 1, 1), (MOST - 255, 1), (MOST - 65535, 1), ((1 << 30) - 1, 2), ((1 << 25) - 1, 64)])
+@pytest.mark.parametrize("total,heads", [(MOST - 1, 1), (MOST - 255, 1), (MOST - 65535, 1), (MOST - 4097 * 32, 1), ((1 << 30) - 1, 2),
+                                         ((1 << 25) - 1, 64)])
 def test_rows_of_nearly_2_31(op, total, heads):
     b = batch(n_seqs=1, total=total, cu_seqlens=1 << 20)
-    refused(op, "total * q_heads must be below 2^31 - 65536", c=cache(kv_heads=1), b=b, q=queries(q_heads=heads))
+    refused(op, "total * q_heads must be below 2^31 - 2^18", c=cache(kv_heads=1), b=b, q=queries(q_heads=heads))
 
 
 def workspace(seqs, n, tokens, heads=8, group=8, d=128, max_q=None, max_len=None):
